@@ -371,6 +371,144 @@ qkr_status rms_norm_fp8(void *stream, const void *x, void *residual, const void 
                         int64_t x_stride, int64_t res_stride, int64_t out_stride, float eps);
 
 /* ------------------------------------------------------------------------
+ * The cache the rotated rows are stored in, and the attention that reads it.
+ * ------------------------------------------------------------------------ */
+
+/* How a cache holds its rows. */
+enum {
+    /* bf16 rows as rope_set_rows writes them: element d of a head row is the
+     * d-th bf16 of it. */
+    QKR_CACHE_BF16 = 0,
+    /* 4 bits an element.  32 consecutive elements of a head row share one
+     * scale s, a bf16 number of at most 5 significant bits; an element is
+     * held as a code c in 0..15 and stands for (c - 8) * s.  A 3-bit integer
+     * times 5 significant bits has 8, so every value the cache stands for is
+     * a bf16 number exactly and reading it back rounds nothing.  Layout of
+     * the D/2 code bytes of a head row, chosen so that a lane of the attention
+     * kernels finds its matrix-instruction operands side by side:
+     *   K rows: element d = 32w + 8c + i (i < 8) is nibble i (low nibble of
+     *           byte 0 first) of the 4-byte word at byte c*(D/8) + 4w;
+     *   V rows: element d = 32w + 4g + i (i < 4) is nibble i of the 2-byte
+     *           word at byte g*(D/16) + 2w.
+     * The D/32 scales of a head row are consecutive bf16 numbers. */
+    QKR_CACHE_Q4 = 1
+};
+
+/* A paged cache of K and V rows.  Row r of page p, head h starts at
+ * base + p*page_stride + r*row_stride + h*head_stride, all strides in bytes
+ * (any order of the axes; rows of different (p, r, h) must not overlap).
+ * k, v hold the rows (QKR_CACHE_BF16: D bf16; QKR_CACHE_Q4: D/2 code bytes);
+ * k_scale, v_scale the scales of QKR_CACHE_Q4 (NULL and ignored otherwise).
+ * The flat row index of rope_set_rows and cache_set_rows_q4 is p*page_size + r.
+ *   page_size   tokens of a page, a multiple of 16, 16 <= page_size <= 65536.
+ *   D           QKR_CACHE_BF16: a multiple of 8, 8 <= D <= 128;
+ *               QKR_CACHE_Q4: 64 or 128.
+ * Alignment: k, v and their strides multiples of 16 bytes; k_scale, v_scale
+ * and their strides multiples of D/16 bytes. */
+typedef struct qkr_cache_plane {
+    void *base;
+    int64_t page_stride, row_stride, head_stride;
+} qkr_cache_plane;
+typedef struct qkr_cache_desc {
+    int32_t format;      /* QKR_CACHE_* */
+    int32_t page_size;
+    int64_t n_pages;
+    int64_t Hkv;
+    int64_t D;
+    qkr_cache_plane k, v, k_scale, v_scale;
+} qkr_cache_desc;
+
+/*
+ * cache_attention -- causal attention of new tokens over a paged cache, with
+ * an optional sliding window and first tokens that stay visible.  Sequence b
+ * has the new tokens cu_q[b] .. cu_q[b+1]-1 of q (n of them; 1 each in a
+ * decode step, a prompt or a part of one otherwise) and lens[b] tokens in the
+ * cache, the new ones included (stored before this call, by rope_set_rows or
+ * cache_set_rows_q4).  New token i sits at position p = lens[b] - n + i and
+ * sees the cached tokens j <= p with
+ *     window == 0,  or  p - j < window,  or  j < n_sink.
+ * With s_j = scale * (q . k_j), m = max s_j, l = sum exp(s_j - m) over the
+ * visible j:   out = sum exp(s_j - m) v_j / l,   lse = m + ln(l).
+ * A token that sees nothing (p < 0) gets out = 0 and lse = -infinity.  Query
+ * head h reads KV head h / (Hq / Hkv).  Token j of sequence b is row
+ * j % page_size of page page_table[b][j / page_size].
+ *
+ * What a token does not see never reaches its result, whatever it holds
+ * (infinities and NaN included); pages that no new token of a sequence sees
+ * are not read and their table entries may be anything.  Rows of q from
+ * cu_q[B] on are not read, and those of out and lse left as they were.
+ *
+ *   q                bf16 device [T, Hq, D], strides in elements (multiples
+ *                    of 8), 16-byte aligned.
+ *   out              bf16 device [T, Hq, D], heads dense, 16-byte aligned,
+ *                    token stride a multiple of 8.  Must not overlap any input.
+ *   lse              nullable fp32 device [T, Hq].
+ *   page_table       int32 device [B, table_stride]; entry [b][i] is the page of
+ *                    tokens i*page_size ... of sequence b.
+ *   lens             int32 device [B];  cu_q int32 device [B + 1], nondecreasing.
+ *   max_q, max_len   host bounds of the new tokens of a sequence and of lens[b];
+ *                    max_len <= table_stride * page_size.  They set the launch
+ *                    shape only, so a captured graph serves any lengths up to them.
+ *   scale            finite.   window, n_sink >= 0.
+ *   workspace        device scratch of cache_attention_workspace() bytes, 16-byte
+ *                    aligned (may be NULL where that is 0).  It carries nothing from
+ *                    call to call; calls that may run at the same time (other
+ *                    streams, graphs replayed side by side) need one each.
+ * What the host cannot see is bounded on the device: a length outside
+ * [0, max_len], a cu_q entry outside [0, T], or more than max_q new tokens is
+ * clamped, a page id outside the cache reads as rows of zeros, and each raises
+ * bit 8 of the device status word.
+ * The maximum, the sum and the output are held in fp32; the weights exp(s - m)
+ * are rounded to bf16 for their product with V, and out once at the end.
+ * Enqueues one kernel, or two: a second where sequences of a few rows and of
+ * many can stand side by side, or where one joins the parts of a long axis.
+ */
+qkr_status cache_attention(void *stream, const qkr_cache_desc *cache, const void *q, void *out,
+                           float *lse, int64_t T, int64_t Hq, int64_t q_tok_stride,
+                           int64_t q_head_stride, int64_t out_tok_stride,
+                           const int32_t *page_table, int64_t table_stride, const int32_t *lens,
+                           const int32_t *cu_q, int64_t B, int64_t max_q, int64_t max_len,
+                           float scale, int64_t window, int64_t n_sink, void *workspace,
+                           int64_t workspace_bytes);
+
+/* Bytes of workspace a cache_attention call of these sizes needs on the
+ * current device (0: none).  Of the cache only format, Hkv and D are read. */
+qkr_status cache_attention_workspace(const qkr_cache_desc *cache, int64_t T, int64_t Hq,
+                                     int64_t B, int64_t max_q, int64_t max_len, int64_t window,
+                                     int64_t n_sink, int64_t *bytes);
+
+/*
+ * cache_set_rows_q4 -- store K and V rows in a QKR_CACHE_Q4 cache (K rotated
+ * already, by mrope_apply say).  Token t goes to flat row row_idx[t].  Per
+ * group of 32 elements: e = the element of largest magnitude (the negative one
+ * when both signs tie), s = e / -8 with its magnitude rounded up to 5 significant
+ * bits (at most 31 * 2^120, so that 8s stays finite), code = clamp(rint(x / s), -8, 7) + 8 (ties to even; 8 where s is 0).
+ * A group with an
+ * infinity or a NaN reads back as NaN throughout.
+ *
+ *   k, v             bf16 device [T, Hkv, D], heads dense, token strides in
+ *                    elements (multiples of 8), 16-byte aligned.
+ *   row_idx          int64 device [T], 8-byte aligned; rows must be distinct
+ *                    within a call.  A row outside the cache is not written and
+ *                    raises bit 4 of the device status word.
+ * The cache must not overlap k, v or row_idx.
+ */
+qkr_status cache_set_rows_q4(void *stream, const qkr_cache_desc *cache, const void *k,
+                             const void *v, const int64_t *row_idx, int64_t T,
+                             int64_t k_tok_stride, int64_t v_tok_stride);
+
+/*
+ * cache_get_rows_q4 -- the rows row_idx[t] of a QKR_CACHE_Q4 cache as the bf16
+ * values they stand for (exact): k_out, v_out bf16 device [T, Hkv, D], heads
+ * dense.  A row may be named more than once.  A row outside the cache reads as
+ * zeros and raises bit 4 of the device status word.  Arguments as
+ * cache_set_rows_q4; the outputs must not overlap each other or any input.
+ */
+qkr_status cache_get_rows_q4(void *stream, const qkr_cache_desc *cache, void *k_out, void *v_out,
+                             const int64_t *row_idx, int64_t T, int64_t k_tok_stride,
+                             int64_t v_tok_stride);
+
+/* ------------------------------------------------------------------------
  * Introspection and debug entry points (used by the tests).
  * ------------------------------------------------------------------------ */
 
@@ -392,7 +530,11 @@ enum {
     QKR_KERNEL_RMS_CLUSTER = 6,    /* one cluster per row */
     QKR_KERNEL_SECTION_MAP = 7,
     QKR_KERNEL_VIT_POSITIONS = 8,
-    QKR_KERNEL_NULL = 9            /* qkr_null_launch */
+    QKR_KERNEL_NULL = 9,           /* qkr_null_launch */
+    QKR_KERNEL_ATTN_ROWS = 10,     /* cache_attention: few rows a sequence, warps own keys */
+    QKR_KERNEL_ATTN_TILES = 11,    /* cache_attention: 128-row tiles on the tensor cores */
+    QKR_KERNEL_SET_ROWS_Q4 = 12,
+    QKR_KERNEL_GET_ROWS_Q4 = 13
 };
 typedef struct qkr_launch_info {
     int32_t kernel;          /* QKR_KERNEL_* */
@@ -413,7 +555,8 @@ typedef struct qkr_launch_info {
                                 were staged per token in shared memory */
     int32_t overlap;         /* 1 if launched with programmatic stream serialisation
                                 (see qkr_launch_overlap) */
-    int32_t stages;          /* streaming kernel: passes in the row ring; else 0 */
+    int32_t stages;          /* streaming kernel: passes in the row ring; cache_attention:
+                                parts the keys of a sequence are split into; else 0 */
     int32_t reserved;        /* 0 */
     int64_t grid;            /* CTAs launched */
     int64_t launches;        /* kernel launches enqueued (0 for an empty call) */
@@ -464,8 +607,11 @@ qkr_status qkr_tune_rope_lanes(int32_t lanes);
 qkr_status qkr_tune_rms(int32_t cluster, int32_t threads);
 
 /* Device status word of the library on the current device (0 = healthy).
- * Bit 4: rope_set_rows met a row index outside the cache (that row was not
- * written).  The word is shared by every call of the process on that device,
+ * Bit 4: rope_set_rows, cache_set_rows_q4 or cache_get_rows_q4 met a row
+ * index outside the cache (that row was not written, or reads as zeros).
+ * Bit 8: cache_attention met a length, offset or page id outside its bounds
+ * (clamped, as stated there).  Bit 16: a bounded wait inside a cache_attention
+ * kernel ran out (its result is not valid).  The word is shared by every call of the process on that device,
  * so a bit cannot be traced to the call that raised it; it stays set until a
  * read with reset != 0 clears it.  The read (and the clear) is one atomic
  * exchange on the device, ordered after the work of every blocking stream:

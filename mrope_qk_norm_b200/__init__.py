@@ -27,12 +27,15 @@ FLAG_EAGER_ROUNDING = 2
 FLAG_INDEPENDENT = 4
 KERNEL_NAMES = {0: "none", 1: "rope_paired", 2: "rope_vector", 3: "rope_exchange",
                 4: "vit_setup", 5: "rms_rows", 6: "rms_cluster", 7: "section_map",
-                8: "vit_positions", 9: "null"}
+                8: "vit_positions", 9: "null", 10: "attn_rows", 11: "attn_tiles",
+                12: "set_rows_q4", 13: "get_rows_q4"}
+CACHE_BF16, CACHE_Q4 = 0, 1
 
 EXPORTS = ("fused_qk_norm_rope", "fused_qkv_norm_rope", "mrope_apply", "rope_set_rows",
            "vit_mrope_setup", "rms_norm_residual", "rms_norm_fp8", "qkr_last_error", "qkr_version", "qkr_last_launch", "qkr_section_map",
            "qkr_vit_positions", "qkr_tune_rope", "qkr_tune_rope_lanes", "qkr_tune_rms", "qkr_device_status",
-           "qkr_launch_overlap", "qkr_null_launch")
+           "qkr_launch_overlap", "qkr_null_launch", "cache_attention",
+           "cache_attention_workspace", "cache_set_rows_q4", "cache_get_rows_q4")
 
 
 class QkrError(RuntimeError):
@@ -60,6 +63,18 @@ class AngleDesc(ctypes.Structure):
                 ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
                 ("table_rows", ctypes.c_int64), ("ld", ctypes.c_int64),
                 ("plane_stride", ctypes.c_int64), ("token_offset", ctypes.c_int64)]
+
+
+class CachePlane(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class CacheDesc(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int64), ("Hkv", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("k", CachePlane), ("v", CachePlane), ("k_scale", CachePlane),
+                ("v_scale", CachePlane)]
 
 
 class LaunchInfo(ctypes.Structure):
@@ -100,6 +115,12 @@ def _load() -> ctypes.CDLL:
         "qkr_launch_overlap": [I32],
         "qkr_device_status": [ctypes.POINTER(ctypes.c_uint32), I32],
         "qkr_null_launch": [V, I64, I32],
+        "cache_attention": [V, ctypes.POINTER(CacheDesc), V, V, V, I64, I64, I64, I64, I64, V,
+                            I64, V, V, I64, I64, I64, F, I64, I64, V, I64],
+        "cache_attention_workspace": [ctypes.POINTER(CacheDesc), I64, I64, I64, I64, I64, I64,
+                                      I64, ctypes.POINTER(I64)],
+        "cache_set_rows_q4": [V, ctypes.POINTER(CacheDesc), V, V, V, I64, I64, I64],
+        "cache_get_rows_q4": [V, ctypes.POINTER(CacheDesc), V, V, V, I64, I64, I64],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -445,3 +466,147 @@ def rms_norm_fp8(x, residual, gamma, out, scale, eps, stream=None):
         _ptr(residual, torch.bfloat16, "residual") if residual is not None else None,
         _ptr(gamma, torch.bfloat16, "gamma"), out.data_ptr(), scale.data_ptr(), R, hidden,
         x.stride(0), residual.stride(0) if residual is not None else 0, out.stride(0), eps))
+
+
+# --------------------------------------------------------------------------
+# the paged cache and the attention that reads it
+# --------------------------------------------------------------------------
+
+def _cache_plane(t, dtype, shape, what) -> CachePlane:
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % what)
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape) or t.stride(3) != 1:
+        raise ValueError("%s must be a [pages, page_size, Hkv, %d] view with a contiguous last "
+                         "dim" % (what, shape[3]))
+    b = t.element_size()
+    return CachePlane(t.data_ptr(), t.stride(0) * b, t.stride(1) * b, t.stride(2) * b)
+
+
+def _cache_common(fmt, k, D, tensors) -> CacheDesc:
+    if k.dim() != 4:
+        raise ValueError("the cache must be [pages, page_size, Hkv, ...] views")
+    if any(t.device != k.device for t in tensors):
+        raise ValueError("the cache tensors must be on one device")
+    d = CacheDesc()
+    d.format = fmt
+    d.n_pages, d.page_size, d.Hkv, d.D = k.shape[0], k.shape[1], k.shape[2], D
+    d._keep = tensors  # the descriptor holds raw pointers into these
+    d._device = k.device
+    return d
+
+
+def cache_desc(k, v) -> CacheDesc:
+    """A paged bf16 cache: k, v [pages, page_size, Hkv, D] views (any strides of the
+    first three axes, D dense).  The cache rope_set_rows writes, [R, Hkv, D],
+    viewed as [R / page_size, page_size, Hkv, D]."""
+    d = _cache_common(CACHE_BF16, k, k.shape[-1], (k, v))
+    d.k = _cache_plane(k, torch.bfloat16, k.shape, "k")
+    d.v = _cache_plane(v, torch.bfloat16, k.shape, "v")
+    return d
+
+
+def cache_desc_q4(k, k_scale, v, v_scale) -> CacheDesc:
+    """A paged 4-bit cache: k, v uint8 [pages, page_size, Hkv, D/2] code views,
+    k_scale, v_scale bf16 [pages, page_size, Hkv, D/32] (any strides of the first
+    three axes; storage ordered [pages, Hkv, page_size, ...] keeps a head's rows
+    of a page together, which the attention reads best).  include/qkr.h states
+    the format."""
+    D = 2 * k.shape[-1]
+    d = _cache_common(CACHE_Q4, k, D, (k, k_scale, v, v_scale))
+    scales = tuple(k.shape[:3]) + (D // 32,)
+    d.k = _cache_plane(k, torch.uint8, k.shape, "k")
+    d.v = _cache_plane(v, torch.uint8, k.shape, "v")
+    d.k_scale = _cache_plane(k_scale, torch.bfloat16, scales, "k_scale")
+    d.v_scale = _cache_plane(v_scale, torch.bfloat16, scales, "v_scale")
+    return d
+
+
+def _on_device(cache: CacheDesc, tensors):
+    for name, t in tensors:
+        if t is not None and t.device != cache._device:
+            raise ValueError("%s must be on the cache's device %s" % (name, cache._device))
+    return torch.cuda.device(cache._device)
+
+
+def cache_attention_workspace(q, cache: CacheDesc, batch, max_q, max_len, window=0,
+                              n_sink=0) -> int:
+    """Bytes of workspace cache_attention needs for q [T, Hq, D] and these sizes."""
+    n = ctypes.c_int64(0)
+    with _on_device(cache, (("q", q),)):
+        _check(_lib.cache_attention_workspace(ctypes.byref(cache), q.shape[0], q.shape[1], batch,
+                                              max_q, max_len, window, n_sink, ctypes.byref(n)))
+    return int(n.value)
+
+
+def cache_attention(q, cache: CacheDesc, out, page_table, lens, cu_q, max_q, max_len, scale=None,
+                    window=0, n_sink=0, lse=None, workspace=None, stream=None):
+    """Causal attention of the new tokens q [T, Hq, D] over a paged cache.
+
+    out: [T, Hq, D] bf16 (heads dense); page_table int32 [B, pages], lens int32
+    [B], cu_q int32 [B + 1]; lse: fp32 [T, Hq] or None; workspace: uint8, at least
+    cache_attention_workspace(...) bytes (None where that is 0); scale defaults to
+    D ** -0.5.  include/qkr.h states what a token sees."""
+    if q.dim() != 3 or q.stride(2) != 1 or q.shape[2] != cache.D:
+        raise ValueError("q must be [T, Hq, %d] with a contiguous last dim" % cache.D)
+    if out.shape != q.shape or out.stride(2) != 1 or (out.shape[1] > 1 and
+                                                      out.stride(1) != out.shape[2]):
+        raise ValueError("out must have q's shape and dense heads")
+    T, Hq, D = q.shape
+    B = lens.shape[0]
+    if lens.dim() != 1 or cu_q.dim() != 1 or cu_q.shape[0] != B + 1 or page_table.dim() != 2 or \
+            page_table.shape[0] != B:
+        raise ValueError("lens must be [B], cu_q [B + 1], page_table [B, pages]")
+    if (B > 1 and lens.stride(0) != 1) or cu_q.stride(0) != 1 or \
+            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("lens, cu_q and the rows of page_table must be contiguous")
+    if B > 1 and page_table.stride(0) < page_table.shape[1]:
+        raise ValueError("the rows of page_table must not overlap")
+    if max_len > page_table.shape[1] * cache.page_size:
+        raise ValueError("max_len %d exceeds the %d tokens of a page_table row"
+                         % (max_len, page_table.shape[1] * cache.page_size))
+    if lse is not None and (lse.shape != q.shape[:2] or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous [T, Hq] tensor")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    tensors = (("q", q), ("out", out), ("page_table", page_table), ("lens", lens),
+               ("cu_q", cu_q), ("lse", lse), ("workspace", workspace))
+    with _on_device(cache, tensors):
+        _check(_lib.cache_attention(
+            _stream(stream), ctypes.byref(cache), _ptr(q, torch.bfloat16, "q"),
+            _ptr(out, torch.bfloat16, "out"), _ptr(lse, torch.float32, "lse"), T, Hq,
+            q.stride(0), q.stride(1) if Hq > 1 else D, out.stride(0) if T > 1 else Hq * D,
+            _ptr(page_table, torch.int32, "page_table"),
+            page_table.stride(0) if B > 1 else page_table.shape[1],
+            _ptr(lens, torch.int32, "lens"), _ptr(cu_q, torch.int32, "cu_q"), B, max_q, max_len,
+            D ** -0.5 if scale is None else scale, window, n_sink, _ptr(workspace),
+            workspace.numel() * workspace.element_size() if workspace is not None else 0))
+
+
+def _rows_q4(fn, k, v, cache, row_idx, stream):
+    for name, t in (("k", k), ("v", v)):
+        if t.dim() != 3 or tuple(t.shape[1:]) != (cache.Hkv, cache.D) or t.stride(2) != 1 or \
+                (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+            raise ValueError("%s must be [T, %d, %d] with dense heads" % (name, cache.Hkv, cache.D))
+    T = k.shape[0]
+    if v.shape[0] != T or row_idx.dim() != 1 or row_idx.shape[0] != T or \
+            (T > 1 and row_idx.stride(0) != 1):
+        raise ValueError("k, v and row_idx must name the same T tokens, row_idx contiguous")
+    dense = cache.Hkv * cache.D
+    with _on_device(cache, (("k", k), ("v", v), ("row_idx", row_idx))):
+        _check(fn(_stream(stream), ctypes.byref(cache), _ptr(k, torch.bfloat16, "k"),
+                  _ptr(v, torch.bfloat16, "v"), _ptr(row_idx, torch.int64, "row_idx"), T,
+                  k.stride(0) if T > 1 else dense, v.stride(0) if T > 1 else dense))
+
+
+def cache_set_rows_q4(k, v, cache: CacheDesc, row_idx, stream=None):
+    """Store K and V rows [T, Hkv, D] bf16 (K rotated already) in the 4-bit cache:
+    token t in flat row row_idx[t] = page * page_size + row (int64, distinct)."""
+    _rows_q4(_lib.cache_set_rows_q4, k, v, cache, row_idx, stream)
+
+
+def cache_get_rows_q4(cache: CacheDesc, row_idx, k_out, v_out, stream=None):
+    """The flat rows row_idx [T] of the 4-bit cache as the bf16 values they stand
+    for: k_out, v_out [T, Hkv, D] bf16."""
+    _rows_q4(_lib.cache_get_rows_q4, k_out, v_out, cache, row_idx, stream)

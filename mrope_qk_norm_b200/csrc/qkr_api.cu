@@ -11,6 +11,7 @@
 #include <cstdio>
 #include <string>
 
+#include "cache_internal.cuh"
 #include "qkr_internal.cuh"
 
 namespace qkr {
@@ -44,6 +45,29 @@ qkr_status cuda_result(cudaError_t e, const char *what)
     g_error.clear();
     return QKR_OK;
 }
+
+}  // namespace
+
+namespace qkr {
+qkr_status api_fail(qkr_status st, const char *fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_error = buf;
+    return st;
+}
+qkr_status api_done(const LaunchRecord &rec)
+{
+    g_error.clear();
+    g_last = rec;
+    return QKR_OK;
+}
+}  // namespace qkr
+
+namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
