@@ -1,5 +1,6 @@
 // cache_api.cu -- C ABI of the paged cache: validation, launch shapes, launch.
 
+#include <cfloat>
 #include <climits>
 #include <cmath>
 
@@ -180,8 +181,10 @@ struct Plan {
     int64_t ws_bytes = 0;
 };
 
-void shape(const Sizes &s, int block_rows, int tile, int64_t slots, int min_split, int64_t lo,
-           int64_t hi, qkr::AttnParams *p, int64_t *grid, int64_t *ws)
+// Blocks of a launch that serves sequences of up to `hi` rows, and the tiles
+// a block can have.
+int64_t blocks(const Sizes &s, int block_rows, int tile, int64_t lo, int64_t hi,
+               qkr::AttnParams *p)
 {
     const int64_t G = s.Hq / s.Hkv;
     p->rows = block_rows;
@@ -194,30 +197,30 @@ void shape(const Sizes &s, int block_rows, int tile, int64_t slots, int min_spli
     p->direct = s.B * per_seq <= by_total;
     p->blocks_max = (int)per_seq;
     p->n_blocks = p->direct ? s.B * per_seq : by_total;
-    // keys a block can see, in tiles (the window and the sinks may each start inside one)
+    // the window and the sinks may each start inside a tile
     int64_t keys = s.max_len;
     if (s.window && s.window + s.n_sink + block_rows / G + 1 < keys)
         keys = s.window + s.n_sink + block_rows / G + 1;
-    const int64_t tiles = keys / tile + (s.window ? 3 : 1);
-    // One wave of equal parts where that is little work; else parts small
-    // enough that six waves or so even out the lengths.
-    const int64_t items = p->n_blocks * s.Hkv;
-    const int64_t share = (items * tiles + slots - 1) / slots;
-    const int64_t fine = 1024 / tile;
-    int64_t split = share <= fine ? share : (share / 6 > fine ? share / 6 : fine);
-    if (split < min_split)
-        split = min_split;
-    split = (split + 3) / 4 * 4;
+    return keys / tile + (s.window ? 3 : 1);
+}
+
+// Cuts the axis into parts of `split` tiles, 1024 at most.
+void cut(const Sizes &s, int64_t tiles, int64_t split, qkr::AttnParams *p, int64_t *ws)
+{
     if (tiles > split * 1024)
         split = (tiles + 1023) / 1024;
-    int64_t n = (tiles + split - 1) / split;
+    const int64_t n = (tiles + split - 1) / split;
     p->split_tiles = (int)split;
     p->nsplit = (int)n;
-    *grid = items * n;
     const int64_t need = n > 1 ? n * s.T * s.Hq * (s.D + 2) * 4 : 0;
     if (need > *ws)
         *ws = need;
 }
+
+// Sequences of up to kFewRows rows go to the rows kernel, longer ones to the
+// tiles kernel; both run where a call can hold both kinds.  One sequence, or
+// as many new tokens as every sequence having max_q would make, is one kind.
+constexpr int64_t kFewRows = 16;
 
 qkr_status make_plan(const Sizes &s, Plan *plan)
 {
@@ -225,12 +228,33 @@ qkr_status make_plan(const Sizes &s, Plan *plan)
     qkr_status st = sm_count(&sms);
     if (st != QKR_OK)
         return st;
-    const int64_t G = s.Hq / s.Hkv;
-    int64_t grid = 0;
-    plan->rows = true;
-    shape(s, s.max_q * G <= 8 ? 8 : 16, 16, (int64_t)sms * 3, 8, 0, INT_MAX, &plan->pr, &grid,
-          &plan->ws_bytes);
-    if (grid > INT_MAX / 64)
+    const int64_t G = s.Hq / s.Hkv, most = s.max_q * G;
+    plan->tiles = most > kFewRows;
+    plan->rows = !plan->tiles || (s.B > 1 && s.T < s.B * s.max_q && G <= kFewRows);
+    if (plan->rows) {
+        qkr::AttnParams &p = plan->pr;
+        const int64_t cap = plan->tiles ? kFewRows : INT_MAX;
+        const int64_t tiles = blocks(s, (most < cap ? most : cap) <= 8 ? 8 : 16, 16, 0, cap, &p);
+        // One wave of equal parts where that is little work; else parts of 1024
+        // keys or more, six waves or so, which evens out the lengths.
+        const int64_t slots = (int64_t)sms * 3, items = p.n_blocks * s.Hkv;
+        const int64_t share = (items * tiles + slots - 1) / slots;
+        int64_t split = share <= 64 ? share : (share / 6 > 64 ? share / 6 : 64);
+        split = split < 8 ? 8 : (split + 3) / 4 * 4;
+        cut(s, tiles, split, &p, &plan->ws_bytes);
+    }
+    if (plan->tiles) {
+        qkr::AttnParams &p = plan->pt;
+        const int64_t tiles = blocks(s, 256, 128, plan->rows ? kFewRows : 0, INT_MAX, &p);
+        // A block's keys are cut only where the blocks alone do not fill the
+        // SMs: a part costs 256 partial rows written and read again.
+        const int64_t items = p.n_blocks * s.Hkv;
+        const int64_t want = items >= sms ? 1 : (2 * sms + items - 1) / items;
+        int64_t split = (tiles + want - 1) / want;
+        cut(s, tiles, split < 4 ? 4 : split, &p, &plan->ws_bytes);
+    }
+    if ((plan->rows && plan->pr.n_blocks * s.Hkv * plan->pr.nsplit > INT_MAX / 256) ||
+        (plan->tiles && plan->pt.n_blocks * s.Hkv * plan->pt.nsplit > INT_MAX / 256))
         return api_fail(QKR_ERR_UNSUPPORTED, "the call needs more blocks than a launch takes");
     return QKR_OK;
 }
@@ -353,7 +377,9 @@ qkr_status cache_attention(void *stream, const qkr_cache_desc *cache, const void
         p.ws_ml = reinterpret_cast<float2 *>(p.ws_o + (int64_t)p.nsplit * s.T * s.Hq * s.D);
         p.status = status;
         const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-        e = qkr::launch_attn_rows(p, q4, cs, &rec);
+        if (which && p.scale_log2 == 0.f)
+            p.scale_log2 = FLT_MIN;  // masked scores are -infinity times the scale
+        e = which ? qkr::launch_attn_tiles(p, q4, cs, &rec) : qkr::launch_attn_rows(p, q4, cs, &rec);
         if (e != cudaSuccess)
             return cuda_fail(e, "cache attention launch");
         if (p.nsplit > 1) {

@@ -247,6 +247,7 @@ __device__ __forceinline__ void attn_emit(const AttnParams &p, const AttnBlock &
 
 // Launchers (one kernel each).
 cudaError_t launch_attn_rows(const AttnParams &p, int q4, cudaStream_t stream, LaunchRecord *rec);
+cudaError_t launch_attn_tiles(const AttnParams &p, int q4, cudaStream_t stream, LaunchRecord *rec);
 cudaError_t launch_attn_join(const AttnParams &p, cudaStream_t stream);
 cudaError_t launch_set_rows_q4(const CacheView &c, const __nv_bfloat16 *k, const __nv_bfloat16 *v,
                                const int64_t *rows, int64_t T, int64_t k_ts, int64_t v_ts,
