@@ -498,46 +498,57 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         __syncwarp();
     } else if (!Q4 && warp == 9) {
         // ================================================ TMA
-        if (lane == 0) {
-            const int page_keys = p.c.page_size;
-            bool ok = true;
-            int it = 0, edges = 0;
-            for (; it < 2 * nt && ok; ++it) {
-                const int st = it % NST;
-                if (it >= NST) {
-                    ok = bar_wait(&sh.empty[st], (it / NST - 1) & 1, &sh.abort);
-                    if (!ok)
-                        break;
-                }
-                const int j0 = k.tile_at(i0 + (it >> 1)) * kTile;
-                const bool is_v = it & 1;
-                // the values of a tile that not every row sees go past a clearing warp
-                uint64_t *bar = &sh.raw[st];
-                if (is_v && !attn_all_see(p, k, j0, kTile))
-                    bar = &sh.land[edges++ & 3];
+        // A lane owns one copy of a tile: `box` keys, 64 dims.  It looks its page
+        // up once for K and V and asks for the next tile's before it waits.
+        const int copies = kTile / map.box * Lay::kHalves;
+        const int hf = lane % Lay::kHalves, c = lane / Lay::kHalves * map.box;
+        const bool mine = lane < copies;
+        auto look = [&](int j, int *page, int *row) {
+            // a copy no row sees any key of reads zeros: a page past the last
+            const int a = k.tile_at(i0 + j) * kTile + c, z = a + map.box;
+            *page = -1;
+            if (mine && j < nt && ((a < k.hi && z > k.lo) || a < k.sink))
+                *page = attn_page(p, k.b, a, hf == 0);
+            if (*page < 0)
+                *page = p.c.n_pages;
+            *row = a % p.c.page_size;
+        };
+        int page, row, page_next, row_next;
+        look(0, &page, &row);
+        bool ok = true;
+        int it = 0, edges = 0;
+        for (; it < 2 * nt; ++it) {
+            const int st = it % NST;
+            const bool is_v = it & 1;
+            if (!is_v)
+                look((it >> 1) + 1, &page_next, &row_next);
+            if (it >= NST)
+                ok = bar_wait(&sh.empty[st], (it / NST - 1) & 1, &sh.abort);
+            if (!__all_sync(0xffffffffu, ok))
+                break;
+            // the values of a tile that not every row sees go past a clearing warp
+            uint64_t *bar = &sh.raw[st];
+            if (is_v && !attn_all_see(p, k, k.tile_at(i0 + (it >> 1)) * kTile, kTile))
+                bar = &sh.land[edges++ & 3];
+            if (lane == 0)
                 bar_expect(bar, Lay::kStageBytes);
-                const CUtensorMap *tm = is_v ? &map.v : &map.k;
+            __syncwarp();
+            if (mine) {
                 const int ar = is_v ? map.axis_row_v : map.axis_row_k;
                 const int ah = is_v ? map.axis_head_v : map.axis_head_k;
-                for (int c = 0; c < kTile; c += map.box) {
-                    // a copy no row sees any key of reads zeros: a page past the last
-                    const int a = j0 + c, z = a + map.box;
-                    int page = -1;
-                    if ((a < k.hi && z > k.lo) || a < k.sink)
-                        page = attn_page(p, k.b, a, true);
-                    if (page < 0)
-                        page = p.c.n_pages;
-                    const int row = a % page_keys;
-                    const int c1 = ar == 1 ? row : (ah == 1 ? kvh : page);
-                    const int c2 = ar == 2 ? row : (ah == 2 ? kvh : page);
-                    const int c3 = ar == 3 ? row : (ah == 3 ? kvh : page);
-#pragma unroll
-                    for (int hf = 0; hf < Lay::kHalves; ++hf)
-                        tma_load(tm, smem_u32(ring + st * Lay::kStageBytes + hf * kTile * 128) +
-                                         c * 128, bar, 64 * hf, c1, c2, c3);
-                }
+                tma_load(is_v ? &map.v : &map.k,
+                         smem_u32(ring + st * Lay::kStageBytes + hf * kTile * 128) + c * 128, bar,
+                         64 * hf, ar == 1 ? row : (ah == 1 ? kvh : page),
+                         ar == 2 ? row : (ah == 2 ? kvh : page),
+                         ar == 3 ? row : (ah == 3 ? kvh : page));
             }
-            // no copy is left in flight
+            if (is_v) {
+                page = page_next;
+                row = row_next;
+            }
+        }
+        // no copy is left in flight
+        if (lane == 0) {
             for (int i = it > NST ? it - NST : 0; i < it; ++i)
                 for (uint32_t n = 0; n < kWaitLimit && !bar_try(&sh.raw[i % NST], (i / NST) & 1); ++n) {
                 }
