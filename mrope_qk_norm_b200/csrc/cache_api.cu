@@ -235,13 +235,22 @@ qkr_status make_plan(const Sizes &s, Plan *plan)
         qkr::AttnParams &p = plan->pr;
         const int64_t cap = plan->tiles ? kFewRows : INT_MAX;
         const int64_t tiles = blocks(s, (most < cap ? most : cap) <= 8 ? 8 : 16, 16, 0, cap, &p);
-        // One wave of equal parts where that is little work; else parts of 1024
-        // keys or more, six waves or so, which evens out the lengths.
-        const int64_t slots = (int64_t)sms * 3, items = p.n_blocks * s.Hkv;
-        const int64_t share = (items * tiles + slots - 1) / slots;
-        int64_t split = share <= 64 ? share : (share / 6 > 64 ? share / 6 : 64);
-        split = split < 8 ? 8 : (split + 3) / 4 * 4;
-        cut(s, tiles, split, &p, &plan->ws_bytes);
+        const int64_t items = p.n_blocks * s.Hkv;   // one block a sequence
+        const int64_t slots = (int64_t)sms * qkr::attn_rows_resident(s.D, p.rows, s.q4);
+        // A cluster a block, as large as leaves a warp two tiles and the clusters
+        // room, where a warp then has at most 6 tiles.  Else even shares, of no
+        // less than 8 tiles.
+        p.nsplit = 1;
+        int64_t size = 1;
+        while (size < 8 && tiles > size * 8 && items * size * 2 <= slots)
+            size *= 2;
+        if (tiles <= size * 4 * 6 && items * size <= 2 * slots) {
+            p.cluster = (int)size;
+        } else {
+            p.ctas = (int)slots;
+            p.split_tiles = 8;
+            plan->ws_bytes = slots * (2 * p.rows * (s.D + 2) * 4 + (int64_t)sizeof(qkr::AttnSpan));
+        }
     }
     if (plan->tiles) {
         qkr::AttnParams &p = plan->pt;
@@ -253,7 +262,7 @@ qkr_status make_plan(const Sizes &s, Plan *plan)
         int64_t split = (tiles + want - 1) / want;
         cut(s, tiles, split < 4 ? 4 : split, &p, &plan->ws_bytes);
     }
-    if ((plan->rows && plan->pr.n_blocks * s.Hkv * plan->pr.nsplit > INT_MAX / 256) ||
+    if ((plan->rows && plan->pr.n_blocks * s.Hkv > INT_MAX / 256) ||
         (plan->tiles && plan->pt.n_blocks * s.Hkv * plan->pt.nsplit > INT_MAX / 256))
         return api_fail(QKR_ERR_UNSUPPORTED, "the call needs more blocks than a launch takes");
     return QKR_OK;
@@ -374,7 +383,11 @@ qkr_status cache_attention(void *stream, const qkr_cache_desc *cache, const void
         p.n_sink = (int)s.n_sink;
         p.scale_log2 = (float)((double)scale * 1.4426950408889634);
         p.ws_o = static_cast<float *>(workspace);
-        p.ws_ml = reinterpret_cast<float2 *>(p.ws_o + (int64_t)p.nsplit * s.T * s.Hq * s.D);
+        const int64_t kept = p.ctas ? 2 * (int64_t)p.ctas * p.rows : (int64_t)p.nsplit * s.T * s.Hq;
+        p.ws_ml = reinterpret_cast<float2 *>(p.ws_o + kept * s.D);
+        p.ws_span = reinterpret_cast<qkr::AttnSpan *>(p.ws_ml + kept);
+        const uint64_t page_tiles = view.page_size / 16;
+        p.page_recip = (((uint64_t)1 << 38) + page_tiles - 1) / page_tiles;
         p.status = status;
         const cudaStream_t cs = static_cast<cudaStream_t>(stream);
         if (which && p.scale_log2 == 0.f)
@@ -382,7 +395,7 @@ qkr_status cache_attention(void *stream, const qkr_cache_desc *cache, const void
         e = which ? qkr::launch_attn_tiles(p, q4, cs, &rec) : qkr::launch_attn_rows(p, q4, cs, &rec);
         if (e != cudaSuccess)
             return cuda_fail(e, "cache attention launch");
-        if (p.nsplit > 1) {
+        if (which && p.nsplit > 1) {
             e = qkr::launch_attn_join(p, cs);
             if (e != cudaSuccess)
                 return cuda_fail(e, "cache attention join launch");

@@ -19,6 +19,15 @@ struct CacheView {
     int Hkv, D;
 };
 
+// A block whose keys several CTAs of the rows kernel share.
+struct AttnSpan {
+    int b, kvh;     // b < 0: none begins here
+    int parts;      // CTAs that share it
+    int slot;       // the first one's slot; the others' are their first
+    int n, L;
+    int64_t t0;
+};
+
 // One cache_attention call.  The queries of a sequence that share a KV head
 // are numbered as rows r = i*G + g (new token i, g-th query head of the KV
 // head), and a block is `rows` consecutive ones: its keys are loaded once for
@@ -45,8 +54,16 @@ struct AttnParams {
     int tile;                // keys of a tile: 16 or 128
     int split_tiles;         // tiles of a part of a block's keys
     int nsplit;              // parts at most
-    float *ws_o;             // [nsplit][T*Hq][D] partial outputs (not divided by l)
-    float2 *ws_ml;           // [nsplit][T*Hq] their maximum (log2 units) and sum
+    uint64_t page_recip;     // rows kernel: ceil(2^38 / (tiles of a page))
+    int ctas;                // rows kernel: CTAs that share all keys evenly; 0: a cluster a block
+    int cluster;             // CTAs of such a cluster
+    // Partial outputs (not divided by l), their maxima (log2 units) and sums.
+    // Tiles kernel: [nsplit][T*Hq][D] and [nsplit][T*Hq].  Rows kernel: a CTA's
+    // first and last piece, [2*ctas][rows][D] and [2*ctas][rows], and what the
+    // CTA's last piece begins, [ctas].
+    float *ws_o;
+    float2 *ws_ml;
+    struct AttnSpan *ws_span;
     unsigned *status;
 };
 
@@ -82,24 +99,54 @@ __device__ __forceinline__ int attn_blocks_of(const AttnParams &p, int n)
     return r > p.rows_lo && r <= p.rows_hi ? (int)((r + p.rows - 1) / p.rows) : 0;
 }
 
+// Block `blk` of sequence b (n new tokens from t0 on) and what it sees.
+__device__ __forceinline__ AttnBlock attn_block_at(const AttnParams &p, int b, int blk, int n,
+                                                   int64_t t0, bool bad)
+{
+    AttnBlock k;
+    int L = p.lens[b];
+    if (L < 0 || L > p.max_len) {
+        bad = true;
+        L = L < 0 ? 0 : p.max_len;
+    }
+    if (bad && (threadIdx.x & 31) == 0)
+        atomicOr(p.status, kStatusBounds);
+    k.b = b;
+    k.t0 = t0;
+    k.n = n;
+    k.L = L;
+    k.row0 = blk * p.rows;
+    k.nrows = min(p.rows, n * p.G - k.row0);
+    k.p_first = L - n + k.row0 / p.G;
+    k.p_last = L - n + (k.row0 + k.nrows - 1) / p.G;
+    k.hi = max(0, k.p_last + 1);
+    k.lo = p.window ? max(0, k.p_first - p.window + 1) : 0;
+    k.lo = min(k.lo, k.hi);
+    k.sink = min(p.n_sink, k.lo);
+    k.c_sink = (k.sink + p.tile - 1) / p.tile;
+    k.c0 = max(k.lo / p.tile, k.c_sink);
+    const int c1 = (k.hi + p.tile - 1) / p.tile;
+    k.ntiles = k.c_sink + max(0, c1 - k.c0);
+    return k;
+}
+
 // The block of block index `idx`, computed by a whole warp.  Where the blocks
 // are not laid out per sequence, each lane counts those of one sequence and
 // the warp adds them up, 32 sequences at a time.
 __device__ __forceinline__ AttnBlock attn_block(const AttnParams &p, int64_t idx)
 {
-    AttnBlock k;
-    k.b = -1;
-    k.ntiles = 0;
-    k.nrows = 0;
-    int b = -1, blk = 0, nblk = 0;
+    AttnBlock none;
+    none.b = -1;
+    int b = -1, blk = 0, nblk = 0, n_of = 0;
+    int64_t t0_of = 0;
     bool bad = false;
     if (p.direct) {
         b = (int)(idx / p.blocks_max);
         blk = (int)(idx % p.blocks_max);
-        k.n = attn_seq(p, b, &k.t0, &bad);
-        nblk = attn_blocks_of(p, k.n);
+        n_of = attn_seq(p, b, &t0_of, &bad);
+        nblk = attn_blocks_of(p, n_of);
         if (blk >= nblk)
-            return k;
+            return none;
     } else {
         const int lane = threadIdx.x & 31;
         int64_t before = 0;
@@ -124,41 +171,18 @@ __device__ __forceinline__ AttnBlock attn_block(const AttnParams &p, int64_t idx
                 b = b0 + src;
                 nblk = __shfl_sync(0xffffffffu, mine, src);
                 blk = (int)(idx - before - (__shfl_sync(0xffffffffu, sum, src) - nblk));
-                k.n = __shfl_sync(0xffffffffu, n, src);
-                k.t0 = __shfl_sync(0xffffffffu, t0, src);
+                n_of = __shfl_sync(0xffffffffu, n, src);
+                t0_of = __shfl_sync(0xffffffffu, t0, src);
                 bad = __shfl_sync(0xffffffffu, (int)mbad, src) != 0;
                 break;
             }
             before += __shfl_sync(0xffffffffu, sum, 31);
         }
         if (b < 0)
-            return k;
+            return none;
     }
     // the last blocks of a sequence see most keys: they go first
-    blk = nblk - 1 - blk;
-    int L = p.lens[b];
-    if (L < 0 || L > p.max_len) {
-        bad = true;
-        L = L < 0 ? 0 : p.max_len;
-    }
-    if (bad && (threadIdx.x & 31) == 0)
-        atomicOr(p.status, kStatusBounds);
-    k.b = b;
-    k.L = L;
-    k.row0 = blk * p.rows;
-    const int total = k.n * p.G;
-    k.nrows = min(p.rows, total - k.row0);
-    k.p_first = L - k.n + k.row0 / p.G;
-    k.p_last = L - k.n + (k.row0 + k.nrows - 1) / p.G;
-    k.hi = max(0, k.p_last + 1);
-    k.lo = p.window ? max(0, k.p_first - p.window + 1) : 0;
-    k.lo = min(k.lo, k.hi);
-    k.sink = min(p.n_sink, k.lo);
-    k.c_sink = (k.sink + p.tile - 1) / p.tile;
-    k.c0 = max(k.lo / p.tile, k.c_sink);
-    const int c1 = (k.hi + p.tile - 1) / p.tile;
-    k.ntiles = k.c_sink + max(0, c1 - k.c0);
-    return k;
+    return attn_block_at(p, b, nblk - 1 - blk, n_of, t0_of, bad);
 }
 
 // Does the token at position pos see key j?
@@ -245,7 +269,10 @@ __device__ __forceinline__ void attn_emit(const AttnParams &p, const AttnBlock &
             empty ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
 }
 
-// Launchers (one kernel each).
+// CTAs of the even-shares rows kernel an SM holds.
+int attn_rows_resident(int64_t D, int rows, int q4);
+
+// Launchers.
 cudaError_t launch_attn_rows(const AttnParams &p, int q4, cudaStream_t stream, LaunchRecord *rec);
 cudaError_t launch_attn_tiles(const AttnParams &p, int q4, cudaStream_t stream, LaunchRecord *rec);
 cudaError_t launch_attn_join(const AttnParams &p, cudaStream_t stream);
