@@ -396,7 +396,7 @@ enum {
 
 /* A paged cache of K and V rows.  Row r of page p, head h starts at
  * base + p*page_stride + r*row_stride + h*head_stride, all strides in bytes
- * (any order of the axes; rows of different (p, r, h) must not overlap).
+ * (any order of the axes, page and row strides below 2^32; rows of different (p, r, h) must not overlap).
  * k, v hold the rows (QKR_CACHE_BF16: D bf16; QKR_CACHE_Q4: D/2 code bytes);
  * k_scale, v_scale the scales of QKR_CACHE_Q4 (NULL and ignored otherwise).
  * The flat row index of rope_set_rows and cache_set_rows_q4 is p*page_size + r.

@@ -54,6 +54,9 @@ qkr_status check_plane(const char *name, const qkr_cache_plane &in, const qkr_ca
         if (use[i] % align)
             return api_fail(QKR_ERR_UNSUPPORTED, "cache %s: strides must be multiples of %lld bytes",
                             name, (long long)align);
+        if (i < 2 && use[i] >= (int64_t)1 << 32)
+            return api_fail(QKR_ERR_UNSUPPORTED, "cache %s: page and row strides must be below 2^32 "
+                            "bytes", name);
         if (use[i] > ((int64_t)1 << 50) / extent[i])
             return api_fail(QKR_ERR_INVALID_ARG, "cache %s exceeds the address range", name);
     }

@@ -37,8 +37,10 @@
 // 4 bits: a nibble n becomes the bf16 number 128 + n by one AND-OR on two
 // nibbles at a time.  For K the products run on 128 + n against an accumulator
 // that starts at -136 * (sum of q), per group of 32 dims, and the group's scale
-// multiplies the sum in fp32.  For V, 136 is subtracted (exact) and the scale
-// goes onto the weight, group by group, before its one rounding.
+// multiplies the sum in fp32.  For V the scale goes onto the weight, group by
+// group, before its one rounding, and a second product takes -136 times the
+// same rounded weights off again, tile by tile, so the offset never builds up
+// in the sum: two matrix instructions in place of eight subtractions.
 
 #include <cooperative_groups.h>
 
@@ -52,22 +54,33 @@ namespace qkr {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr uint32_t kMinus136 = 0xc308c308u;  // bf16 pair
 constexpr float kSlack = 8.f;  // log2 units the reference may lag behind the maximum
+
+// Tiles a warp takes together.
+constexpr int rows_unroll(int dp, bool q4) { return q4 || dp == 64 ? 2 : 1; }
 
 // CTAs of the even-shares kernel an SM holds (by registers).
 constexpr int rows_ctas(int dp, int nt, bool q4)
 {
-    return nt == 2 ? (dp == 64 && !q4 ? 3 : 2) : (dp == 64 ? 4 : 3);
+    return nt == 2 ? 2 : (dp == 64 && q4 ? 4 : 3);
 }
 
+// d = a b + c on 16 x 8 x 16.
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1)
+                                         uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
+                                         float c2, float c3)
 {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    mma16816(d, a0, a1, a2, a3, b0, b1, d[0], d[1], d[2], d[3]);
 }
 
 // Transpose of an 8x8 matrix of 16-bit elements spread over the warp.
@@ -126,6 +139,14 @@ struct LanePtr {
     const uint8_t *k, *v, *ks, *vs;
 };
 
+__device__ __forceinline__ const uint8_t *tile_ptr(const uint8_t *lane, const CachePlane &pl,
+                                                   const Tile &at)
+{
+    // page and row strides are below 2^32
+    return lane + (uint64_t)(uint32_t)at.page * (uint32_t)pl.ps +
+           (uint64_t)(uint32_t)at.row * (uint32_t)pl.rs;
+}
+
 // Loads of a tile (16 keys from a multiple of 16, so within one page).  Keys
 // no row of the block sees read as zeros: what lies there may be anything.
 template <int DP, bool Q4>
@@ -133,18 +154,20 @@ __device__ __forceinline__ void load_k(KTile<DP, Q4> &t, const AttnParams &p, co
                                        const LanePtr &lp, const Tile &at, bool all)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const uint8_t *src = lp.k + at.page * p.c.k.ps + at.row * p.c.k.rs;
-    const uint8_t *ss = Q4 ? lp.ks + at.page * p.c.ks.ps + at.row * p.c.ks.rs : nullptr;
+    const uint8_t *src = tile_ptr(lp.k, p.c.k, at);
+    const uint8_t *ss = Q4 ? tile_ptr(lp.ks, p.c.ks, at) : nullptr;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const bool ok = all || (at.page >= 0 && attn_block_sees(k, at.j0 + g + 8 * i));
         if constexpr (Q4) {
+            if (!all) {
 #pragma unroll
-            for (int w = 0; w < DP / 32; ++w)
-                t.w[i][w] = 0x88888888u;
+                for (int w = 0; w < DP / 32; ++w)
+                    t.w[i][w] = 0x88888888u;
 #pragma unroll
-            for (int w = 0; w < DP / 64; ++w)
-                t.s[i][w] = 0u;
+                for (int w = 0; w < DP / 64; ++w)
+                    t.s[i][w] = 0u;
+            }
             if (ok) {
                 ld_words<DP / 32>(t.w[i], src + 8 * i * p.c.k.rs);
                 ld_words<DP / 64>(t.s[i], ss + 8 * i * p.c.ks.rs);
@@ -167,7 +190,7 @@ __device__ __forceinline__ void load_v(VTile<DP, Q4> &t, const AttnParams &p, co
                                        const LanePtr &lp, const Tile &at, bool all)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const uint8_t *src = lp.v + at.page * p.c.v.ps + at.row * p.c.v.rs;
+    const uint8_t *src = tile_ptr(lp.v, p.c.v, at);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int x = (i & 1) + 8 * (i >> 1);       // key 2c + x
@@ -175,7 +198,8 @@ __device__ __forceinline__ void load_v(VTile<DP, Q4> &t, const AttnParams &p, co
         if constexpr (Q4) {
 #pragma unroll
             for (int w = 0; w < DP / 64; ++w)
-                t.w[i][w] = 0x88888888u;
+                if (!all)
+                    t.w[i][w] = 0x88888888u;
             if (ok)
                 ld_words<DP / 64>(t.w[i], src + x * p.c.v.rs);
         } else {
@@ -190,12 +214,13 @@ __device__ __forceinline__ void load_v(VTile<DP, Q4> &t, const AttnParams &p, co
         }
     }
     if constexpr (Q4) {
-        const uint8_t *ss = lp.vs + at.page * p.c.vs.ps + at.row * p.c.vs.rs;
+        const uint8_t *ss = tile_ptr(lp.vs, p.c.vs, at);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
             for (int w = 0; w < DP / 64; ++w)
-                t.s[i][w] = 0u;
+                if (!all)
+                    t.s[i][w] = 0u;
             if (all || (at.page >= 0 && attn_block_sees(k, at.j0 + g + 8 * i)))
                 ld_words<DP / 64>(t.s[i], ss + 8 * i * p.c.vs.rs);
         }
@@ -218,7 +243,7 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
 {
     constexpr int KS = DP / 16;       // k steps of S^T, m tiles of O^T
     constexpr int GR = DP / 32;       // 4-bit groups of a row
-    constexpr int U = Q4 ? 2 : 1;     // tiles a warp takes together
+    constexpr int U = rows_unroll(DP, Q4);   // tiles a warp takes together
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 
     // ---- the warp's first tiles are asked for before anything else
@@ -253,9 +278,22 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
             t->page = -1;
         }
     };
-    // all keys of the tile are seen by some row, and its page exists
-    auto whole = [&](const Tile &t) {
-        return t.page >= 0 && t.j0 + 16 <= k.hi && (t.j0 >= k.lo || t.j0 + 16 <= k.sink);
+    // Tiles [in0, in1) of the piece: every row sees all their keys.
+    const int in0 = k.c_sink +
+                    (p.window ? max(0, (max(0, k.p_last - p.window + 1) + 15) / 16 - k.c0) : 0);
+    const int in1 = min(i1, k.c_sink + (k.p_first + 1) / 16 - k.c0);
+    // two copies of the loads: with and without a question per key
+    auto get_k = [&](KTile<DP, Q4> &t, const Tile &at, bool plain) {
+        if (plain)
+            load_k<DP, Q4>(t, p, k, lp, at, true);
+        else
+            load_k<DP, Q4>(t, p, k, lp, at, false);
+    };
+    auto get_v = [&](VTile<DP, Q4> &t, const Tile &at, bool plain) {
+        if (plain)
+            load_v<DP, Q4>(t, p, k, lp, at, true);
+        else
+            load_v<DP, Q4>(t, p, k, lp, at, false);
     };
     KTile<DP, Q4> kt[U];
     VTile<DP, Q4> vt[U];
@@ -286,11 +324,16 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
                 qv[n][w] = ld_stream(src + 32 * w);
         }
     }
+    bool full = i >= in0 && i + U <= in1, plain = full;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         admit(&cur[u]);
-        load_k<DP, Q4>(kt[u], p, k, lp, cur[u], whole(cur[u]));
-        load_v<DP, Q4>(vt[u], p, k, lp, cur[u], whole(cur[u]));
+        plain &= cur[u].page >= 0;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        get_k(kt[u], cur[u], plain);
+        get_v(vt[u], cur[u], plain);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -360,8 +403,9 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
                     const float s1 = bf16_at(kt[u].s[1][w / 2], w & 1);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        float d[4] = {qs[n][0][w], qs[n][1][w], qs[n][0][w], qs[n][1][w]};
-                        mma16816(d, a[0], a[1], a[2], a[3], qf[n][2 * w][0], qf[n][2 * w][1]);
+                        float d[4];
+                        mma16816(d, a[0], a[1], a[2], a[3], qf[n][2 * w][0], qf[n][2 * w][1],
+                                 qs[n][0][w], qs[n][1][w], qs[n][0][w], qs[n][1][w]);
                         mma16816(d, a[4], a[5], a[6], a[7], qf[n][2 * w + 1][0],
                                  qf[n][2 * w + 1][1]);
                         s[u][n][0] = fmaf(d[0], s0, s[u][n][0]);
@@ -380,41 +424,60 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
                                  qf[n][x][1]);
             }
         }
-        const bool more = i + kWarps * U < i1;
-        Tile was[U];
+        const int in = i + kWarps * U;
+        const bool more = in < i1, was_full = full;
+        int was[U];
+        plain = full = in >= in0 && in + U <= in1;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            was[u] = cur[u];
+            was[u] = cur[u].j0;
             cur[u] = next[u];
             admit(&cur[u]);
+            plain &= cur[u].page >= 0;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
             if (more)
-                load_k<DP, Q4>(kt[u], p, k, lp, cur[u], whole(cur[u]));
-            locate(i + 2 * kWarps * U + u, &next[u]);
+                get_k(kt[u], cur[u], plain);
+            locate(in + kWarps * U + u, &next[u]);
         }
 
         bool raise = false;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const bool full = attn_all_see(p, k, was[u].j0, 16);
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 4; ++e)
                     s[u][n][e] *= p.scale_log2;
-                    if (!full && !attn_sees(p, pos[n][e & 1], was[u].j0 + g + 8 * (e >> 1)))
-                        s[u][n][e] = -INFINITY;
-                    raise |= s[u][n][e] > m[n][e & 1] + kSlack;
-                }
-            }
-            if (!full && k.p_first != k.p_last) {
+        if (!was_full) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!attn_sees(p, pos[n][e & 1], was[u] + g + 8 * (e >> 1)))
+                            s[u][n][e] = -INFINITY;
                 // a key only some rows see must not reach the others through 0 * NaN
+                if (k.p_first != k.p_last)
 #pragma unroll
-                for (int y = 0; y < (Q4 ? 2 : 4); ++y)
+                    for (int y = 0; y < (Q4 ? 2 : 4); ++y)
 #pragma unroll
-                    for (int w = 0; w < DP / (Q4 ? 64 : 16); ++w)
-                        poison |= nonfinite2(Q4 ? vt[u].s[y][w] : vt[u].w[y][w]);
+                        for (int w = 0; w < DP / (Q4 ? 64 : 16); ++w)
+                            poison |= nonfinite2(Q4 ? vt[u].s[y][w] : vt[u].w[y][w]);
             }
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float mx = s[0][n][e];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    mx = fmaxf(mx, fmaxf(s[u][n][e], s[u][n][e + 2]));
+                raise |= mx > m[n][e] + kSlack;
+            }
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -470,13 +533,14 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
                     const uint32_t hi = __byte_perm(vt[u].w[2][w / 2], vt[u].w[3][w / 2], sel);
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const uint32_t a0 = sub136(nibbles(lo, 2 * y));
-                        const uint32_t a1 = sub136(nibbles(lo, 2 * y + 1));
-                        const uint32_t a2 = sub136(nibbles(hi, 2 * y));
-                        const uint32_t a3 = sub136(nibbles(hi, 2 * y + 1));
+                        const uint32_t a0 = nibbles(lo, 2 * y), a1 = nibbles(lo, 2 * y + 1);
+                        const uint32_t a2 = nibbles(hi, 2 * y), a3 = nibbles(hi, 2 * y + 1);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
+                        for (int n = 0; n < NT; ++n) {
                             mma16816(o[n][2 * w + y], a0, a1, a2, a3, b[n][0], b[n][1]);
+                            mma16816(o[n][2 * w + y], kMinus136, kMinus136, kMinus136, kMinus136,
+                                     b[n][0], b[n][1]);
+                        }
                     }
                 }
             } else {
@@ -498,7 +562,7 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
                 }
             }
             if (more)
-                load_v<DP, Q4>(vt[u], p, k, lp, cur[u], whole(cur[u]));
+                get_v(vt[u], cur[u], plain);
         }
     }
 

@@ -78,7 +78,7 @@ def test_attention_refusals(status, kw):
     (U, dict(fmt=qkr.CACHE_Q4, D=96)), (U, dict(fmt=qkr.CACHE_Q4, D=32)),
     (E, dict(k__base=0)), (U, dict(v__base=BASE + 8)), (U, dict(k__row_stride=250)),
     (U, dict(k__row_stride=264)), (U, dict(v__head_stride=0)), (U, dict(k__page_stride=-4096)),
-    (E, dict(k__page_stride=1 << 51)),
+    (U, dict(k__page_stride=1 << 32)), (U, dict(v__row_stride=1 << 32)), (E, dict(k__head_stride=1 << 50)),
     (E, dict(fmt=qkr.CACHE_Q4, k_scale__base=0)), (U, dict(fmt=qkr.CACHE_Q4, v_scale__base=BASE + 2)),
 ])
 def test_cache_refusals(status, kw):
