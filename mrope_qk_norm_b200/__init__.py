@@ -146,7 +146,9 @@ def lib() -> ctypes.CDLL:
 
 class _LazyLib:
     def __getattr__(self, name):
-        return getattr(lib(), name)
+        fn = getattr(lib(), name)
+        setattr(self, name, fn)   # found at once from the next call on
+        return fn
 
 
 _lib = _LazyLib()
@@ -493,7 +495,8 @@ def _cache_common(fmt, k, D, tensors) -> CacheDesc:
     d.format = fmt
     d.n_pages, d.page_size, d.Hkv, d.D = k.shape[0], k.shape[1], k.shape[2], D
     d._keep = tensors  # the descriptor holds raw pointers into these
-    d._device = k.device
+    d._device, d._page, d._H, d._D = k.device, k.shape[1], k.shape[2], D
+    d._ref = ctypes.byref(d)
     return d
 
 
@@ -523,20 +526,41 @@ def cache_desc_q4(k, k_scale, v, v_scale) -> CacheDesc:
     return d
 
 
-def _on_device(cache: CacheDesc, tensors):
-    for name, t in tensors:
-        if t is not None and t.device != cache._device:
-            raise ValueError("%s must be on the cache's device %s" % (name, cache._device))
-    return torch.cuda.device(cache._device)
+# A decode step is a few microseconds on the device, so these calls keep their
+# host side short: every property of a tensor is read once, and the device is
+# switched only when it is not the current one.
+
+def _launch(device, stream, fn, *args):
+    """fn(stream, *args) with `device` current, on `stream` or its current stream."""
+    i = device.index
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(i)
+    else:
+        s = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+    if torch._C._cuda_getDevice() == i:
+        status = fn(s, *args)
+    else:
+        with torch.cuda.device(i):
+            status = fn(s, *args)
+    if status != QKR_OK:
+        _check(status)
+
+
+def _arg(t, dtype, device, what) -> int:
+    if t.dtype is not dtype:
+        raise ValueError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    if t.device != device:
+        raise ValueError("%s must be on the cache's device %s" % (what, device))
+    return t.data_ptr()
 
 
 def cache_attention_workspace(q, cache: CacheDesc, batch, max_q, max_len, window=0,
                               n_sink=0) -> int:
     """Bytes of workspace cache_attention needs for q [T, Hq, D] and these sizes."""
     n = ctypes.c_int64(0)
-    with _on_device(cache, (("q", q),)):
-        _check(_lib.cache_attention_workspace(ctypes.byref(cache), q.shape[0], q.shape[1], batch,
-                                              max_q, max_len, window, n_sink, ctypes.byref(n)))
+    T, Hq, _ = q.shape
+    _launch(cache._device, None, lambda s, *a: _lib.cache_attention_workspace(*a), cache._ref, T,
+            Hq, batch, max_q, max_len, window, n_sink, ctypes.byref(n))
     return int(n.value)
 
 
@@ -548,56 +572,70 @@ def cache_attention(q, cache: CacheDesc, out, page_table, lens, cu_q, max_q, max
     [B], cu_q int32 [B + 1]; lse: fp32 [T, Hq] or None; workspace: uint8, at least
     cache_attention_workspace(...) bytes (None where that is 0); scale defaults to
     D ** -0.5.  include/qkr.h states what a token sees."""
-    if q.dim() != 3 or q.stride(2) != 1 or q.shape[2] != cache.D:
-        raise ValueError("q must be [T, Hq, %d] with a contiguous last dim" % cache.D)
-    if out.shape != q.shape or out.stride(2) != 1 or (out.shape[1] > 1 and
-                                                      out.stride(1) != out.shape[2]):
+    dev = cache._device
+    D = cache._D
+    qs, os_ = q.shape, out.shape
+    if len(qs) != 3 or qs[2] != D:
+        raise ValueError("q must be [T, Hq, %d] with a contiguous last dim" % D)
+    T, Hq, _ = qs
+    qt, qh, qd = q.stride()
+    if qd != 1:
+        raise ValueError("q must be [T, Hq, %d] with a contiguous last dim" % D)
+    if os_ != qs:
         raise ValueError("out must have q's shape and dense heads")
-    T, Hq, D = q.shape
-    B = lens.shape[0]
-    if lens.dim() != 1 or cu_q.dim() != 1 or cu_q.shape[0] != B + 1 or page_table.dim() != 2 or \
-            page_table.shape[0] != B:
+    ot, oh, od = out.stride()
+    if od != 1 or (Hq > 1 and oh != D):
+        raise ValueError("out must have q's shape and dense heads")
+    ls, cs, ts = lens.shape, cu_q.shape, page_table.shape
+    if len(ls) != 1 or len(cs) != 1 or len(ts) != 2 or cs[0] != ls[0] + 1 or ts[0] != ls[0]:
         raise ValueError("lens must be [B], cu_q [B + 1], page_table [B, pages]")
-    if (B > 1 and lens.stride(0) != 1) or cu_q.stride(0) != 1 or \
-            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+    B, cols = ts
+    tb, tc = page_table.stride()
+    if (B > 1 and lens.stride(0) != 1) or cu_q.stride(0) != 1 or (cols > 1 and tc != 1):
         raise ValueError("lens, cu_q and the rows of page_table must be contiguous")
-    if B > 1 and page_table.stride(0) < page_table.shape[1]:
-        raise ValueError("the rows of page_table must not overlap")
-    if max_len > page_table.shape[1] * cache.page_size:
+    if B > 1:
+        if tb < cols:
+            raise ValueError("the rows of page_table must not overlap")
+    else:
+        tb = cols
+    if max_len > cols * cache._page:
         raise ValueError("max_len %d exceeds the %d tokens of a page_table row"
-                         % (max_len, page_table.shape[1] * cache.page_size))
-    if lse is not None and (lse.shape != q.shape[:2] or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous [T, Hq] tensor")
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    tensors = (("q", q), ("out", out), ("page_table", page_table), ("lens", lens),
-               ("cu_q", cu_q), ("lse", lse), ("workspace", workspace))
-    with _on_device(cache, tensors):
-        _check(_lib.cache_attention(
-            _stream(stream), ctypes.byref(cache), _ptr(q, torch.bfloat16, "q"),
-            _ptr(out, torch.bfloat16, "out"), _ptr(lse, torch.float32, "lse"), T, Hq,
-            q.stride(0), q.stride(1) if Hq > 1 else D, out.stride(0) if T > 1 else Hq * D,
-            _ptr(page_table, torch.int32, "page_table"),
-            page_table.stride(0) if B > 1 else page_table.shape[1],
-            _ptr(lens, torch.int32, "lens"), _ptr(cu_q, torch.int32, "cu_q"), B, max_q, max_len,
-            D ** -0.5 if scale is None else scale, window, n_sink, _ptr(workspace),
-            workspace.numel() * workspace.element_size() if workspace is not None else 0))
+                         % (max_len, cols * cache._page))
+    i32, bf = torch.int32, torch.bfloat16
+    lse_p = ws_p = ws_n = 0
+    if lse is not None:
+        if lse.shape != qs[:2] or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous [T, Hq] tensor")
+        lse_p = _arg(lse, torch.float32, dev, "lse")
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        ws_n = workspace.nbytes
+        ws_p = _arg(workspace, workspace.dtype, dev, "workspace")
+    _launch(dev, stream, _lib.cache_attention, cache._ref, _arg(q, bf, dev, "q"),
+            _arg(out, bf, dev, "out"), lse_p, T, Hq, qt, qh if Hq > 1 else D,
+            ot if T > 1 else Hq * D, _arg(page_table, i32, dev, "page_table"), tb,
+            _arg(lens, i32, dev, "lens"), _arg(cu_q, i32, dev, "cu_q"), B, max_q, max_len,
+            D ** -0.5 if scale is None else scale, window, n_sink, ws_p, ws_n)
 
 
 def _rows_q4(fn, k, v, cache, row_idx, stream):
-    for name, t in (("k", k), ("v", v)):
-        if t.dim() != 3 or tuple(t.shape[1:]) != (cache.Hkv, cache.D) or t.stride(2) != 1 or \
-                (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-            raise ValueError("%s must be [T, %d, %d] with dense heads" % (name, cache.Hkv, cache.D))
-    T = k.shape[0]
-    if v.shape[0] != T or row_idx.dim() != 1 or row_idx.shape[0] != T or \
-            (T > 1 and row_idx.stride(0) != 1):
-        raise ValueError("k, v and row_idx must name the same T tokens, row_idx contiguous")
-    dense = cache.Hkv * cache.D
-    with _on_device(cache, (("k", k), ("v", v), ("row_idx", row_idx))):
-        _check(fn(_stream(stream), ctypes.byref(cache), _ptr(k, torch.bfloat16, "k"),
-                  _ptr(v, torch.bfloat16, "v"), _ptr(row_idx, torch.int64, "row_idx"), T,
-                  k.stride(0) if T > 1 else dense, v.stride(0) if T > 1 else dense))
+    dev, H, D = cache._device, cache._H, cache._D
+    ks, vs, n = k.shape, v.shape, row_idx.shape
+    if len(ks) != 3 or ks[1] != H or ks[2] != D or vs != ks or len(n) != 1 or n[0] != ks[0]:
+        raise ValueError("k and v must be [T, %d, %d], row_idx [T]" % (H, D))
+    T = ks[0]
+    kt, kh, kd = k.stride()
+    vt, vh, vd = v.stride()
+    if kd != 1 or vd != 1 or (H > 1 and (kh != D or vh != D)):
+        raise ValueError("k and v must have dense heads")
+    if T > 1 and row_idx.stride(0) != 1:
+        raise ValueError("row_idx must be contiguous")
+    if T <= 1:
+        kt = vt = H * D
+    bf = torch.bfloat16
+    _launch(dev, stream, fn, cache._ref, _arg(k, bf, dev, "k"), _arg(v, bf, dev, "v"),
+            _arg(row_idx, torch.int64, dev, "row_idx"), T, kt, vt)
 
 
 def cache_set_rows_q4(k, v, cache: CacheDesc, row_idx, stream=None):

@@ -1,5 +1,6 @@
 // cache_api.cu -- C ABI of the paged cache: validation, launch shapes, launch.
 
+#include <atomic>
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -142,13 +143,38 @@ qkr_status cuda_fail(cudaError_t e, const char *what)
     return api_fail(QKR_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-qkr_status sm_count(int *sms)
+// What a call needs to know of the current device; asked of the driver once.
+constexpr int kMaxDevices = 64;
+struct Device {
+    std::atomic<int> sms{0};
+    std::atomic<unsigned *> status{nullptr};
+};
+Device g_devices[kMaxDevices];
+
+qkr_status current_device(int *sms, unsigned **status)
 {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess)
+    if (e != cudaSuccess)
+        return cuda_fail(e, "device query");
+    if (dev < 0 || dev >= kMaxDevices)
+        return api_fail(QKR_ERR_UNSUPPORTED, "device %d: at most %d devices", dev, kMaxDevices);
+    Device &d = g_devices[dev];
+    *sms = d.sms.load(std::memory_order_relaxed);
+    if (*sms == 0) {
         e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-    return e == cudaSuccess ? QKR_OK : cuda_fail(e, "device query");
+        if (e != cudaSuccess)
+            return cuda_fail(e, "device query");
+        d.sms.store(*sms, std::memory_order_relaxed);
+    }
+    *status = d.status.load(std::memory_order_relaxed);
+    if (!*status) {
+        e = qkr::device_status_address(status);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "status word");
+        d.status.store(*status, std::memory_order_relaxed);
+    }
+    return QKR_OK;
 }
 
 // Sizes every cache_attention launch shape follows from.
@@ -182,6 +208,7 @@ struct Plan {
     bool rows = false, tiles = false;
     qkr::AttnParams pr = {}, pt = {};
     int64_t ws_bytes = 0;
+    unsigned *status = nullptr;
 };
 
 // Blocks of a launch that serves sequences of up to `hi` rows, and the tiles
@@ -228,7 +255,7 @@ constexpr int64_t kFewRows = 16;
 qkr_status make_plan(const Sizes &s, Plan *plan)
 {
     int sms = 0;
-    qkr_status st = sm_count(&sms);
+    qkr_status st = current_device(&sms, &plan->status);
     if (st != QKR_OK)
         return st;
     const int64_t G = s.Hq / s.Hkv, most = s.max_q * G;
@@ -356,10 +383,7 @@ qkr_status cache_attention(void *stream, const qkr_cache_desc *cache, const void
             return st;
     }
 
-    unsigned *status = nullptr;
-    cudaError_t e = qkr::device_status_address(&status);
-    if (e != cudaSuccess)
-        return cuda_fail(e, "status word");
+    cudaError_t e;
     qkr::LaunchRecord rec;
     for (int which = 0; which < 2; ++which) {
         if (!(which ? plan.tiles : plan.rows))
@@ -391,7 +415,7 @@ qkr_status cache_attention(void *stream, const qkr_cache_desc *cache, const void
         p.ws_span = reinterpret_cast<qkr::AttnSpan *>(p.ws_ml + kept);
         const uint64_t page_tiles = view.page_size / 16;
         p.page_recip = (((uint64_t)1 << 38) + page_tiles - 1) / page_tiles;
-        p.status = status;
+        p.status = plan.status;
         const cudaStream_t cs = static_cast<cudaStream_t>(stream);
         if (which && p.scale_log2 == 0.f)
             p.scale_log2 = FLT_MIN;  // masked scores are -infinity times the scale
@@ -439,9 +463,10 @@ static qkr_status rows_q4(void *stream, const qkr_cache_desc *cache, const void 
     if (!set && (meet(bk, bv) || meet(bk, bi) || meet(bv, bi)))
         return api_fail(QKR_ERR_UNSUPPORTED, "k_out, v_out and row_idx must not overlap");
     unsigned *status = nullptr;
-    cudaError_t e = qkr::device_status_address(&status);
-    if (e != cudaSuccess)
-        return cuda_fail(e, "status word");
+    int sms = 0;
+    if ((st = current_device(&sms, &status)) != QKR_OK)
+        return st;
+    cudaError_t e;
     qkr::LaunchRecord rec;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     auto *kb = static_cast<__nv_bfloat16 *>(const_cast<void *>(k));
