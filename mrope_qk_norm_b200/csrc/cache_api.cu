@@ -4,6 +4,9 @@
 #include <cfloat>
 #include <climits>
 #include <cmath>
+#include <mutex>
+#include <set>
+#include <utility>
 
 #include "cache_internal.cuh"
 
@@ -150,6 +153,9 @@ struct Device {
     std::atomic<unsigned *> status{nullptr};
 };
 Device g_devices[kMaxDevices];
+
+std::mutex g_smem_mu;
+std::set<std::pair<int, const void *>> g_smem;   // kernels allowed, by device
 
 qkr_status current_device(int *sms, unsigned **status)
 {
@@ -300,6 +306,21 @@ qkr_status make_plan(const Sizes &s, Plan *plan)
 
 }  // namespace
 
+cudaError_t qkr::allow_smem(const void *fn, int bytes)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    std::lock_guard<std::mutex> lock(g_smem_mu);
+    if (g_smem.count({dev, fn}))
+        return cudaSuccess;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        g_smem.insert({dev, fn});
+    return e;
+}
+
 extern "C" {
 
 qkr_status cache_attention_workspace(const qkr_cache_desc *cache, int64_t T, int64_t Hq,
@@ -413,6 +434,12 @@ qkr_status cache_attention(void *stream, const qkr_cache_desc *cache, const void
         const int64_t kept = p.ctas ? 2 * (int64_t)p.ctas * p.rows : (int64_t)p.nsplit * s.T * s.Hq;
         p.ws_ml = reinterpret_cast<float2 *>(p.ws_o + kept * s.D);
         p.ws_span = reinterpret_cast<qkr::AttnSpan *>(p.ws_ml + kept);
+        if (q4) {
+            p.dense_scales = 1;
+            for (const qkr::CachePlane *pl : {&view.ks, &view.vs})
+                if (pl->rs != s.D / 16 || pl->hs % 16 || pl->ps % 16 || !aligned(pl->base, 16))
+                    p.dense_scales = 0;
+        }
         const uint64_t page_tiles = view.page_size / 16;
         p.page_recip = (((uint64_t)1 << 38) + page_tiles - 1) / page_tiles;
         p.status = plan.status;

@@ -10,14 +10,20 @@
 //   O^T [16 dims x 8 rows] += V^T [16 x 16 keys] . P^T [16 x 8]
 // The dims of a head may be summed in any order, so a lane takes 16 consecutive
 // bytes of a key's row for its K operand (the matching order of Q is set up
-// once), and for V^T 16 consecutive bytes of each of its four keys, paired key
-// by key with byte permutes.  Keys and values thus go from global memory
-// straight into the operand registers: no shared memory, no barrier, and every
-// warp walks its own keys with its own running maximum.  The next tile's K is
-// requested when this one's has been used and likewise V, so a warp always has
-// about one step of keys in flight: 16 (8 KB) in bf16, 32 (4.5 KB) in 4 bits at D
-// = 128; 12 to 16 warps an SM keep the 40-50 KB in flight that HBM's latency asks
-// for.
+// once), and for V^T the same 16 bytes of each of its four keys, paired key by
+// key with byte permutes.
+//
+// One warp feeds, four compute.  The feeding warp looks the pages up and copies
+// rows by TMA into a ring in shared memory, up to 96 KB ahead; the ring runs on
+// from block to block, so a short sequence costs no pause.  A stage holds a step
+// of every computing warp: one tile of 16 keys in bf16, two in 4 bits (18 KB).
+// Which key of a tile is which row of the operand is free as well; the order
+// below makes the operand loads of eight lanes meet eight different banks in
+// the layout the copies leave.  Where a scale row is not one of a dense run,
+// its 8 (4) bytes come by cp.async.  Before this the warps loaded their own
+// operands into registers (q4_decode_long 141 us: three warps a scheduler, each
+// waiting for its own loads), and with a feeding warp that copied 16 bytes a
+// lane that warp was the bound (decode_long 344 us against 146).
 //
 // Who takes which keys.  Much work: as many CTAs as stay resident, each with the
 // same number of tiles of the row (sequence, KV head, tile), found on the device
@@ -47,24 +53,18 @@
 #include <climits>
 
 #include "cache_attn.cuh"
+#include "cache_tma.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace qkr {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;              // computing warps; one more feeds them
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr uint32_t kWaitLimit = 1u << 21;
 constexpr uint32_t kMinus136 = 0xc308c308u;  // bf16 pair
 constexpr float kSlack = 8.f;  // log2 units the reference may lag behind the maximum
-
-// Tiles a warp takes together.
-constexpr int rows_unroll(int dp, bool q4) { return q4 || dp == 64 ? 2 : 1; }
-
-// CTAs of the even-shares kernel an SM holds (by registers).
-constexpr int rows_ctas(int dp, int nt, bool q4)
-{
-    return nt == 2 ? 2 : (dp == 64 && q4 ? 4 : 3);
-}
 
 // d = a b + c on 16 x 8 x 16.
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -91,219 +91,250 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x)
     return y;
 }
 
-// What a lane holds of a tile of 16 keys.  g = lane / 4, c = lane % 4.
-//   K: keys g and g + 8, dims 32w + 8c .. + 7
-//   V: keys 2c, 2c + 1, 2c + 8, 2c + 9; bf16: dims 64h + 8g .. + 7,
-//      4 bits: dims 32w + 4g .. + 3
-//   scales: keys g and g + 8 of both (the weights are scaled where they are made)
-template <int DP, bool Q4>
-struct KTile {
-    uint32_t w[2][Q4 ? DP / 32 : DP / 8];
-    uint32_t s[2][Q4 ? DP / 64 : 1];
-};
-template <int DP, bool Q4>
-struct VTile {
-    uint32_t w[4][Q4 ? DP / 64 : DP / 16];
-    uint32_t s[2][Q4 ? DP / 64 : 1];
+template <int DP, bool Q4, int NT>
+struct Rows {
+    static constexpr int U = Q4 ? 2 : 1;                    // tiles a warp takes together
+    static constexpr int kKeys = kWarps * U * 16;           // keys of a stage
+    static constexpr int kHalves = DP / 64;
+    static constexpr int kRowPart = Q4 ? DP / 2 : 128;      // bytes of a row in one copy
+    static constexpr int kScale = Q4 ? DP / 16 : 0;         // bytes of its scales
+    static constexpr int kPart = kKeys * (Q4 ? DP / 2 : DP * 2);   // K or V of a stage
+    static constexpr int kStageBytes = 2 * (kPart + kKeys * kScale);
+    static constexpr int kStages = Q4 ? (DP == 64 ? 4 : 3) : (DP == 64 ? 4 : (NT == 1 ? 3 : 2));
+    // CTAs an SM holds (by shared memory and registers)
+    static constexpr int kCtas = DP == 128 ? (Q4 && NT == 1 ? 3 : 2) : (Q4 && NT == 1 ? 4 : 3);
 };
 
-template <int N>
-__device__ __forceinline__ void ld_words(uint32_t *w, const uint8_t *p)
+// After the ring, which the copies want on a 1024-byte boundary.
+template <int DP, int NT>
+struct alignas(16) RowsShared {
+    float o[kWarps][8 * NT][DP + 4];
+    float m[kWarps][8 * NT], l[kWarps][8 * NT];
+    int poison, abort;
+    int scan[kWarps + 1];
+    uint64_t full[4], empty[4];
+};
+
+// The key of a tile that is row `r` of the operand, and where 16-byte chunk `ch`
+// of key t of the stage lies from the start of its K or V part.
+template <int DP, bool Q4>
+__device__ __forceinline__ int key_of(int r)
 {
-    if constexpr (N % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-            const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
-            w[4 * i] = v.x;
-            w[4 * i + 1] = v.y;
-            w[4 * i + 2] = v.z;
-            w[4 * i + 3] = v.w;
-        }
+    // eight 4-bit fields, key of row i in field i; rows 8..15 likewise
+    constexpr uint32_t order = !Q4 ? 0x36147250u         // 0 5 2 7 4 1 6 3
+                                   : (DP == 128 ? 0x65742130u
+                                                : 0x67453210u); // 0 1 2 3 5 4 7 6
+    return (r & 8) + (int)(order >> (4 * (r & 7)) & 7u);
+}
+template <int DP, bool Q4, int KEYS>
+__device__ __forceinline__ int chunk_at(int t, int ch)
+{
+    if constexpr (!Q4)                      // 64 dims of all keys, then the next 64
+        return (ch >> 3) * (KEYS * 128) + t * 128 + (((ch & 7) ^ (t & 7)) << 4);
+    else if constexpr (DP == 128)
+        return t * 64 + ((ch ^ (t >> 1 & 3)) << 4);
+    else
+        return t * 32 + (ch << 4);
+}
+
+__device__ __forceinline__ uint32_t sm_u32(const void *p)
+{
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+template <int N>
+__device__ __forceinline__ void copy_small(uint32_t dst, const void *src, bool take)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N),
+                 "r"(take ? N : 0) : "memory");
+}
+__device__ __forceinline__ void full_when_copied(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void bar_init(uint64_t *bar, int count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(sm_u32(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(sm_u32(bar)),
+                 "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(sm_u32(bar)) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok) : "r"(sm_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+// Bounded; after a wait that ran out no other waits (the result is reported as
+// not valid, nothing is accessed that would not be otherwise).
+__device__ __forceinline__ void bar_wait(uint64_t *bar, uint32_t parity, int *abort)
+{
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        if (bar_try(bar, parity))
+            return;
+        if ((i & 15u) == 15u && *reinterpret_cast<volatile int *>(abort))
+            return;
+    }
+    *reinterpret_cast<volatile int *>(abort) = 1;
+}
+// The computing warps among themselves.
+__device__ __forceinline__ void compute_sync()
+{
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t *w, const uint8_t *p)
+{
+    if constexpr (N == 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
     } else if constexpr (N == 2) {
-        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
         w[0] = v.x;
         w[1] = v.y;
     } else {
-        static_assert(N == 1, "1, 2 or a multiple of 4 words");
-        w[0] = __ldcs(reinterpret_cast<const uint32_t *>(p));
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
     }
 }
 
-// A tile: its first key and its page (-1: reads as zeros), the row in it.
-struct Tile {
-    int j0, page, row;
-};
-
-// A lane's place in the rows of a KV head.
-struct LanePtr {
-    const uint8_t *k, *v, *ks, *vs;
-};
-
-__device__ __forceinline__ const uint8_t *tile_ptr(const uint8_t *lane, const CachePlane &pl,
-                                                   const Tile &at)
+// Untiled copy of a run of scale rows.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
-    // page and row strides are below 2^32
-    return lane + (uint64_t)(uint32_t)at.page * (uint32_t)pl.ps +
-           (uint64_t)(uint32_t)at.row * (uint32_t)pl.rs;
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+        ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
-// Loads of a tile (16 keys from a multiple of 16, so within one page).  Keys
-// no row of the block sees read as zeros: what lies there may be anything.
-template <int DP, bool Q4>
-__device__ __forceinline__ void load_k(KTile<DP, Q4> &t, const AttnParams &p, const AttnBlock &k,
-                                       const LanePtr &lp, const Tile &at, bool all)
+// The feeding warp: tiles [i0, i1) of a block and KV head into the ring, which
+// stands at its stage number `it`.  A lane owns one copy of a stage: the 16 keys
+// of a tile (always within one page), of K or V, 64 dims (bf16) or the codes or
+// the scales (4 bits).
+template <int DP, bool Q4, int NT>
+__device__ __forceinline__ void attn_feed(const AttnParams &p, const CacheMaps &maps,
+                                          const AttnBlock &k, int kvh, int i0, int i1,
+                                          RowsShared<DP, NT> &sh, uint8_t *ring, int *it)
 {
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const uint8_t *src = tile_ptr(lp.k, p.c.k, at);
-    const uint8_t *ss = Q4 ? tile_ptr(lp.ks, p.c.ks, at) : nullptr;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const bool ok = all || (at.page >= 0 && attn_block_sees(k, at.j0 + g + 8 * i));
-        if constexpr (Q4) {
-            if (!all) {
-#pragma unroll
-                for (int w = 0; w < DP / 32; ++w)
-                    t.w[i][w] = 0x88888888u;
-#pragma unroll
-                for (int w = 0; w < DP / 64; ++w)
-                    t.s[i][w] = 0u;
-            }
-            if (ok) {
-                ld_words<DP / 32>(t.w[i], src + 8 * i * p.c.k.rs);
-                ld_words<DP / 64>(t.s[i], ss + 8 * i * p.c.ks.rs);
-            }
-        } else {
-#pragma unroll
-            for (int w = 0; w < DP / 32; ++w) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    t.w[i][4 * w + x] = 0u;
-                if (ok && 32 * w + 8 * c < p.c.D)
-                    ld_words<4>(&t.w[i][4 * w], src + 8 * i * p.c.k.rs + 64 * w);
-            }
-        }
-    }
-}
-
-template <int DP, bool Q4>
-__device__ __forceinline__ void load_v(VTile<DP, Q4> &t, const AttnParams &p, const AttnBlock &k,
-                                       const LanePtr &lp, const Tile &at, bool all)
-{
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const uint8_t *src = tile_ptr(lp.v, p.c.v, at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int x = (i & 1) + 8 * (i >> 1);       // key 2c + x
-        const bool ok = all || (at.page >= 0 && attn_block_sees(k, at.j0 + 2 * c + x));
-        if constexpr (Q4) {
-#pragma unroll
-            for (int w = 0; w < DP / 64; ++w)
-                if (!all)
-                    t.w[i][w] = 0x88888888u;
-            if (ok)
-                ld_words<DP / 64>(t.w[i], src + x * p.c.v.rs);
-        } else {
-#pragma unroll
-            for (int h = 0; h < DP / 64; ++h) {
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    t.w[i][4 * h + y] = 0u;
-                if (ok && 64 * h + 8 * g < p.c.D)
-                    ld_words<4>(&t.w[i][4 * h], src + x * p.c.v.rs + 128 * h);
-            }
-        }
-    }
-    if constexpr (Q4) {
-        const uint8_t *ss = tile_ptr(lp.vs, p.c.vs, at);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int w = 0; w < DP / 64; ++w)
-                if (!all)
-                    t.s[i][w] = 0u;
-            if (all || (at.page >= 0 && attn_block_sees(k, at.j0 + g + 8 * i)))
-                ld_words<DP / 64>(t.s[i], ss + 8 * i * p.c.vs.rs);
-        }
-    }
-}
-
-template <int DP, int NT>
-struct RowsShared {
-    float o[kWarps][8 * NT][DP + 4];
-    float m[kWarps][8 * NT], l[kWarps][8 * NT];
-    int poison;
-    int scan[kWarps];
-};
-
-// The tiles [i0, i1) of a block and KV head by one CTA; each warp's maxima,
-// sums and outputs go to sh.  Ends with a barrier.
-template <int DP, int NT, bool Q4>
-__device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock &k, int kvh, int i0,
-                                           int i1, RowsShared<DP, NT> &sh)
-{
-    constexpr int KS = DP / 16;       // k steps of S^T, m tiles of O^T
-    constexpr int GR = DP / 32;       // 4-bit groups of a row
-    constexpr int U = rows_unroll(DP, Q4);   // tiles a warp takes together
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-
-    // ---- the warp's first tiles are asked for before anything else
-    LanePtr lp;
-    lp.k = p.c.k.base + kvh * p.c.k.hs + g * p.c.k.rs + c * (Q4 ? DP / 8 : 16);
-    lp.v = p.c.v.base + kvh * p.c.v.hs + 2 * c * p.c.v.rs + g * (Q4 ? DP / 16 : 16);
-    lp.ks = lp.vs = nullptr;
-    if constexpr (Q4) {
-        lp.ks = p.c.ks.base + kvh * p.c.ks.hs + g * p.c.ks.rs;
-        lp.vs = p.c.vs.base + kvh * p.c.vs.hs + g * p.c.vs.rs;
-    }
+    using R = Rows<DP, Q4, NT>;
+    constexpr int KINDS = Q4 ? 4 : 2 * R::kHalves;
+    const int lane = threadIdx.x & 31;
+    constexpr int box = 16;
+    const int kind = lane % KINDS, first = lane / KINDS * box;
+    const bool mine = first < R::kKeys;
+    const bool is_v = Q4 ? kind & 1 : kind >= R::kHalves;
+    const bool scales = Q4 && kind >= 2;
+    const int half = Q4 ? 0 : kind % R::kHalves;
+    const CachePlane &sp = is_v ? p.c.vs : p.c.ks;
+    const uint32_t part = is_v ? R::kPart : 0;
+    const uint32_t to = scales ? 2 * R::kPart + (is_v ? R::kKeys * R::kScale : 0) + first * R::kScale
+                               : part + half * (R::kKeys * 128) + first * R::kRowPart;
+    const uint32_t bytes = scales ? box * R::kScale : box * R::kRowPart;
     const int32_t *table = p.table + (int64_t)k.b * p.table_stride;
-    auto locate = [&](int i, Tile *t) {
-        if (i >= i1) {
-            t->j0 = INT_MAX / 2;   // no row sees it
-            t->page = -1;
-            t->row = 0;
+    // this lane's run of keys in the stage at tile i: its page (-1: none; -2: no
+    // key of it is seen by any row) and the row there
+    auto look = [&](int i, int *page, int *row) {
+        *page = -2;
+        *row = 0;
+        i += first / 16;
+        if (!mine || i >= i1)
             return;
-        }
         const int at = k.tile_at(i);
         // division by the tiles of a page: exact for tiles below 2^26
         const int pg = (int)((uint64_t)at * p.page_recip >> 38);
-        t->j0 = at * 16;
-        t->row = t->j0 - pg * p.c.page_size;
-        t->page = table[pg];
+        *row = at * 16 - pg * p.c.page_size;
+        *page = table[pg];
     };
-    // a page id outside the cache
-    auto admit = [&](Tile *t) {
-        if ((unsigned)t->page >= (unsigned)p.c.n_pages) {
-            if (t->j0 < INT_MAX / 2 && lane == 0)
-                atomicOr(p.status, kStatusBounds);
-            t->page = -1;
+    int page, row;
+    look(i0, &page, &row);
+    for (int i = i0; i < i1; i += R::kKeys / 16, ++*it) {
+        const int st = *it % R::kStages;
+        const uint32_t at = sm_u32(ring) + st * R::kStageBytes + to;
+        const uint32_t bar = sm_u32(&sh.full[st]);
+        int page_next, row_next;
+        look(i + R::kKeys / 16, &page_next, &row_next);
+        if (page != -2 && (unsigned)page >= (unsigned)p.c.n_pages) {
+            atomicOr(p.status, kStatusBounds);
+            page = -1;
         }
-    };
-    // Tiles [in0, in1) of the piece: every row sees all their keys.
-    const int in0 = k.c_sink +
-                    (p.window ? max(0, (max(0, k.p_last - p.window + 1) + 15) / 16 - k.c0) : 0);
-    const int in1 = min(i1, k.c_sink + (k.p_first + 1) / 16 - k.c0);
-    // two copies of the loads: with and without a question per key
-    auto get_k = [&](KTile<DP, Q4> &t, const Tile &at, bool plain) {
-        if (plain)
-            load_k<DP, Q4>(t, p, k, lp, at, true);
-        else
-            load_k<DP, Q4>(t, p, k, lp, at, false);
-    };
-    auto get_v = [&](VTile<DP, Q4> &t, const Tile &at, bool plain) {
-        if (plain)
-            load_v<DP, Q4>(t, p, k, lp, at, true);
-        else
-            load_v<DP, Q4>(t, p, k, lp, at, false);
-    };
-    KTile<DP, Q4> kt[U];
-    VTile<DP, Q4> vt[U];
-    Tile cur[U], next[U];
-    int i = i0 + warp * U;
+        if (*it >= R::kStages)
+            bar_wait(&sh.empty[st], (*it / R::kStages - 1) & 1, &sh.abort);
+        __syncwarp();
+        const bool by_bulk = !scales || p.dense_scales;
+        const bool copies = page >= 0 || (page == -1 && !scales);
+        const bool issue = by_bulk && copies;
+        if (scales && p.dense_scales && page == -1)      // scales of a page that does not exist
+            for (int x = 0; x < (int)bytes; x += 16)
+                *reinterpret_cast<uint4 *>(ring + st * R::kStageBytes + to + x) = make_uint4(0, 0, 0, 0);
+        uint32_t total = issue ? bytes : 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        locate(i + u, &cur[u]);
-        locate(i + kWarps * U + u, &next[u]);
+        for (int o = 16; o > 0; o >>= 1)
+            total += __shfl_xor_sync(0xffffffffu, total, o);
+        if (lane == 0)
+            bar_expect(&sh.full[st], total);
+        __syncwarp();
+        if (issue) {
+            if (scales)
+                bulk_load(at, sp.base + kvh * sp.hs + (uint64_t)page * (uint32_t)sp.ps +
+                                  (uint64_t)(uint32_t)row * (uint32_t)sp.rs, bytes, bar);
+            else
+                plane_load(is_v ? maps.v : maps.k, at, bar, 64 * half, row, kvh,
+                           page < 0 ? p.c.n_pages : page);
+        }
+        if constexpr (Q4) {
+            if (!p.dense_scales) {
+                // one row a lane and step, K and V in turn
+                for (int x = lane; x < 2 * R::kKeys; x += 32) {
+                    const int t = x % R::kKeys, own = t / box * KINDS + 2 + x / R::kKeys;
+                    const int pg = __shfl_sync(0xffffffffu, page, own);
+                    const int rw = __shfl_sync(0xffffffffu, row, own) + t % box;
+                    const CachePlane &pl = x < R::kKeys ? p.c.ks : p.c.vs;
+                    const uint8_t *src = pl.base + kvh * pl.hs +
+                                         (pg < 0 ? 0 : (uint64_t)pg * (uint32_t)pl.ps +
+                                                           (uint64_t)(uint32_t)rw * (uint32_t)pl.rs);
+                    copy_small<R::kScale>(sm_u32(ring) + st * R::kStageBytes + 2 * R::kPart +
+                                              x * R::kScale, src, pg >= 0);
+                }
+                full_when_copied(&sh.full[st]);
+            }
+        }
+        page = page_next;
+        row = row_next;
     }
+}
+
+// No copy is left in flight (only a wait that ran out could leave one).
+template <int STAGES, int DP, int NT>
+__device__ __forceinline__ void feed_end(RowsShared<DP, NT> &sh, int it)
+{
+    for (int i = it > STAGES ? it - STAGES : 0; i < it; ++i)
+        for (uint32_t n = 0; n < kWaitLimit && !bar_try(&sh.full[i % STAGES], (i / STAGES) & 1); ++n) {
+        }
+}
+
+// The tiles [i0, i1) of a block and KV head by the computing warps, out of the
+// ring; each warp's maxima, sums and outputs go to sh.  Ends with their barrier.
+template <int DP, int NT, bool Q4>
+__device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock &k, int kvh, int i0,
+                                           int i1, RowsShared<DP, NT> &sh, const uint8_t *ring,
+                                           int *it)
+{
+    using R = Rows<DP, Q4, NT>;
+    constexpr int KS = DP / 16;       // k steps of S^T, m tiles of O^T
+    constexpr int GR = DP / 32;       // 4-bit groups of a row
+    constexpr int U = R::U;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 
     // ---- this block's rows: Q as the B operand, positions of a lane's columns
     uint32_t qf[NT][KS][2];
@@ -323,17 +354,6 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
             if (r < k.nrows && 32 * w + 8 * c < p.c.D)
                 qv[n][w] = ld_stream(src + 32 * w);
         }
-    }
-    bool full = i >= in0 && i + U <= in1, plain = full;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        admit(&cur[u]);
-        plain &= cur[u].page >= 0;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        get_k(kt[u], cur[u], plain);
-        get_v(vt[u], cur[u], plain);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -381,26 +401,48 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
         l[n][0] = l[n][1] = 0.f;
     }
     bool poison = false;
+    // Tiles [in0, in1) of the piece: every row sees all their keys.
+    const int in0 = k.c_sink +
+                    (p.window ? max(0, (max(0, k.p_last - p.window + 1) + 15) / 16 - k.c0) : 0);
+    const int in1 = min(i1, k.c_sink + (k.p_first + 1) / 16 - k.c0);
+    constexpr int KEYS = R::kKeys;
+    const int gk = key_of<DP, Q4>(g);       // the lane's keys: gk, gk + 8 of K and S ...
+    const int vk[2] = {key_of<DP, Q4>(2 * c), key_of<DP, Q4>(2 * c + 1)};   // ... these, + 8 of V
 
-    for (; i < i1; i += kWarps * U) {
+    for (int i = i0 + warp * U; i - warp * U < i1; i += kWarps * U, ++*it) {
+        const int st = *it % R::kStages;
+        bar_wait(&sh.full[st], (*it / R::kStages) & 1, &sh.abort);
+        if (i < i1) {
+        const uint8_t *stage = ring + st * R::kStageBytes;
+        const int t0 = warp * U * 16;           // the warp's first key of the stage
+        const bool full = i >= in0 && i + U <= in1;
+
         // S^T: lane has keys g, g + 8 (elements 0 and 1, 2 and 3) of columns 2c, 2c + 1
         float s[U][NT][4];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            const int tk = t0 + 16 * u + gk;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 s[u][n][0] = s[u][n][1] = s[u][n][2] = s[u][n][3] = 0.f;
             if constexpr (Q4) {
+                uint32_t kw[2][GR], ks[2][GR / 2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int b = c * (DP / 8);
+                    lds_words<GR>(kw[y], stage + chunk_at<DP, Q4, KEYS>(tk + 8 * y, b >> 4) + (b & 15));
+                    lds_words<GR / 2>(ks[y], stage + 2 * R::kPart + (tk + 8 * y) * R::kScale);
+                }
 #pragma unroll
                 for (int w = 0; w < GR; ++w) {
                     uint32_t a[8];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        a[2 * x] = nibbles(kt[u].w[0][w], x);
-                        a[2 * x + 1] = nibbles(kt[u].w[1][w], x);
+                        a[2 * x] = nibbles(kw[0][w], x);
+                        a[2 * x + 1] = nibbles(kw[1][w], x);
                     }
-                    const float s0 = bf16_at(kt[u].s[0][w / 2], w & 1);
-                    const float s1 = bf16_at(kt[u].s[1][w / 2], w & 1);
+                    const float s0 = bf16_at(ks[0][w / 2], w & 1);
+                    const float s1 = bf16_at(ks[1][w / 2], w & 1);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         float d[4];
@@ -416,33 +458,19 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
                 }
             } else {
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int w = 0; w < GR; ++w) {
+                    const uint4 a = *reinterpret_cast<const uint4 *>(stage + chunk_at<DP, Q4, KEYS>(tk, 4 * w + c));
+                    const uint4 b = *reinterpret_cast<const uint4 *>(stage + chunk_at<DP, Q4, KEYS>(tk + 8, 4 * w + c));
 #pragma unroll
-                    for (int x = 0; x < KS; ++x)
-                        mma16816(s[u][n], kt[u].w[0][2 * x], kt[u].w[1][2 * x],
-                                 kt[u].w[0][2 * x + 1], kt[u].w[1][2 * x + 1], qf[n][x][0],
-                                 qf[n][x][1]);
+                    for (int n = 0; n < NT; ++n) {
+                        mma16816(s[u][n], a.x, b.x, a.y, b.y, qf[n][2 * w][0], qf[n][2 * w][1]);
+                        mma16816(s[u][n], a.z, b.z, a.w, b.w, qf[n][2 * w + 1][0],
+                                 qf[n][2 * w + 1][1]);
+                    }
+                }
             }
         }
-        const int in = i + kWarps * U;
-        const bool more = in < i1, was_full = full;
-        int was[U];
-        plain = full = in >= in0 && in + U <= in1;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            was[u] = cur[u].j0;
-            cur[u] = next[u];
-            admit(&cur[u]);
-            plain &= cur[u].page >= 0;
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (more)
-                get_k(kt[u], cur[u], plain);
-            locate(in + kWarps * U + u, &next[u]);
-        }
 
-        bool raise = false;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -450,24 +478,19 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     s[u][n][e] *= p.scale_log2;
-        if (!was_full) {
+        if (!full) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
+                const int j0 = i + u < i1 ? k.tile_at(i + u) * 16 : INT_MAX / 2;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (!attn_sees(p, pos[n][e & 1], was[u] + g + 8 * (e >> 1)))
+                        if (!attn_sees(p, pos[n][e & 1], j0 + gk + 8 * (e >> 1)))
                             s[u][n][e] = -INFINITY;
-                // a key only some rows see must not reach the others through 0 * NaN
-                if (k.p_first != k.p_last)
-#pragma unroll
-                    for (int y = 0; y < (Q4 ? 2 : 4); ++y)
-#pragma unroll
-                        for (int w = 0; w < DP / (Q4 ? 64 : 16); ++w)
-                            poison |= nonfinite2(Q4 ? vt[u].s[y][w] : vt[u].w[y][w]);
             }
         }
+        bool raise = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -517,20 +540,48 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
         // O^T: two rows of dims and one pair of keys per register
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            // the second of two tiles may lie beyond the piece: nothing was copied there
+            if (u && i + u >= i1)
+                break;
+            const uint8_t *vpart = stage + R::kPart;
+            const int tk = t0 + 16 * u, j0 = full ? 0 : k.tile_at(i + u) * 16;
             if constexpr (Q4) {
+                uint32_t vw[4][GR / 2], vs[2][GR / 2];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int b = g * (DP / 16);
+                    lds_words<GR / 2>(
+                        vw[y], vpart + chunk_at<DP, Q4, KEYS>(tk + vk[y & 1] + 8 * (y >> 1), b >> 4) +
+                                   (b & 15));
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                    lds_words<GR / 2>(vs[y], stage + 2 * R::kPart + (KEYS + tk + gk + 8 * y) * R::kScale);
+                if (!full) {
+                    // 0 * NaN: a key no row sees becomes zero; one that only some
+                    // rows see must not reach the others
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int w = 0; w < GR / 2; ++w) {
+                            if (!attn_block_sees(k, j0 + gk + 8 * y))
+                                vs[y][w] = 0u;
+                            poison |= k.p_first != k.p_last && nonfinite2(vs[y][w]);
+                        }
+                }
 #pragma unroll
                 for (int w = 0; w < GR; ++w) {
                     uint32_t b[NT][2];
-                    const float s0 = bf16_at(vt[u].s[0][w / 2], w & 1);
-                    const float s1 = bf16_at(vt[u].s[1][w / 2], w & 1);
+                    const float s0 = bf16_at(vs[0][w / 2], w & 1);
+                    const float s1 = bf16_at(vs[1][w / 2], w & 1);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         b[n][0] = transpose8(pack2(s[u][n][0] * s0, s[u][n][1] * s0));
                         b[n][1] = transpose8(pack2(s[u][n][2] * s1, s[u][n][3] * s1));
                     }
                     const int sel = w & 1 ? 0x7632 : 0x5410;
-                    const uint32_t lo = __byte_perm(vt[u].w[0][w / 2], vt[u].w[1][w / 2], sel);
-                    const uint32_t hi = __byte_perm(vt[u].w[2][w / 2], vt[u].w[3][w / 2], sel);
+                    const uint32_t lo = __byte_perm(vw[0][w / 2], vw[1][w / 2], sel);
+                    const uint32_t hi = __byte_perm(vw[2][w / 2], vw[3][w / 2], sel);
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const uint32_t a0 = nibbles(lo, 2 * y), a1 = nibbles(lo, 2 * y + 1);
@@ -551,19 +602,45 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
                     b[n][1] = transpose8(pack2(s[u][n][2], s[u][n][3]));
                 }
 #pragma unroll
-                for (int w = 0; w < DP / 16; ++w) {
-                    const uint32_t a0 = __byte_perm(vt[u].w[0][w], vt[u].w[1][w], 0x5410);
-                    const uint32_t a1 = __byte_perm(vt[u].w[0][w], vt[u].w[1][w], 0x7632);
-                    const uint32_t a2 = __byte_perm(vt[u].w[2][w], vt[u].w[3][w], 0x5410);
-                    const uint32_t a3 = __byte_perm(vt[u].w[2][w], vt[u].w[3][w], 0x7632);
+                for (int h = 0; h < DP / 64; ++h) {
+                    uint4 v[4];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        mma16816(o[n][w], a0, a1, a2, a3, b[n][0], b[n][1]);
+                    for (int y = 0; y < 4; ++y)
+                        v[y] = *reinterpret_cast<const uint4 *>(
+                            vpart + chunk_at<DP, Q4, KEYS>(tk + vk[y & 1] + 8 * (y >> 1), 8 * h + g));
+                    if (!full) {
+                        // 0 * NaN: a key no row sees becomes zero; one that only
+                        // some rows see must not reach the others
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            if (!attn_block_sees(k, j0 + vk[y & 1] + 8 * (y >> 1)))
+                                v[y] = make_uint4(0, 0, 0, 0);
+                            poison |= k.p_first != k.p_last &&
+                                      (nonfinite2(v[y].x) | nonfinite2(v[y].y) |
+                                       nonfinite2(v[y].z) | nonfinite2(v[y].w));
+                        }
+                    }
+                    const uint32_t q0[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+                    const uint32_t q1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+                    const uint32_t q2[4] = {v[2].x, v[2].y, v[2].z, v[2].w};
+                    const uint32_t q3[4] = {v[3].x, v[3].y, v[3].z, v[3].w};
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t a0 = __byte_perm(q0[w], q1[w], 0x5410);
+                        const uint32_t a1 = __byte_perm(q0[w], q1[w], 0x7632);
+                        const uint32_t a2 = __byte_perm(q2[w], q3[w], 0x5410);
+                        const uint32_t a3 = __byte_perm(q2[w], q3[w], 0x7632);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma16816(o[n][4 * h + w], a0, a1, a2, a3, b[n][0], b[n][1]);
+                    }
                 }
             }
-            if (more)
-                get_v(vt[u], cur[u], plain);
         }
+        }
+        __syncwarp();
+        if (lane == 0)
+            bar_arrive(&sh.empty[st]);
     }
 
     // ---- columns 2c, 2c + 1 of the lane are rows of the block
@@ -591,6 +668,21 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
                 *reinterpret_cast<float2 *>(dst + d) = make_float2(o[n][y][e], o[n][y][e + 2]);
             }
         }
+    }
+    compute_sync();
+}
+
+template <int DP, int NT>
+__device__ __forceinline__ void rows_setup(RowsShared<DP, NT> &sh, int fills)
+{
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 4; ++i) {
+            bar_init(&sh.full[i], fills);
+            bar_init(&sh.empty[i], kWarps);
+        }
+        sh.poison = 0;
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
 }
@@ -630,11 +722,19 @@ __device__ __forceinline__ void attn_piece_row(const AttnParams &p, const AttnBl
 
 // Little work: a cluster shares the tiles of a block and joins them.
 template <int DP, int NT, bool Q4>
-__global__ void __launch_bounds__(32 * kWarps)
-attn_cluster_kernel(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(kThreads)
+attn_cluster_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CacheMaps maps)
 {
     constexpr int E = DP / 32;
-    __shared__ __align__(16) RowsShared<DP, NT> sh;
+    using R = Rows<DP, Q4, NT>;
+    extern __shared__ __align__(1024) uint8_t ring[];
+    auto &sh = *reinterpret_cast<RowsShared<DP, NT> *>(ring + R::kStages * R::kStageBytes);
+    if (sm_u32(ring) & 1023u) {     // the copies' swizzle counts on it
+        if (threadIdx.x == 0)
+            atomicOr(p.status, kStatusWait);
+        return;
+    }
+    rows_setup<DP, NT>(sh, Q4 && !p.dense_scales ? 33 : 1);
     pdl_wait();
     pdl_trigger();
     cg::cluster_group cluster = cg::this_cluster();
@@ -645,13 +745,15 @@ attn_cluster_kernel(const __grid_constant__ AttnParams p)
     const AttnBlock k = attn_block(p, item / p.c.Hkv);
     if (k.b < 0)
         return;     // the whole cluster
-    if (threadIdx.x == 0)
-        sh.poison = 0;
-    __syncthreads();
     const int share = (k.ntiles + size - 1) / size;
     const int i0 = min(k.ntiles, rank * share), i1 = min(k.ntiles, i0 + share);
-    attn_piece<DP, NT, Q4>(p, k, kvh, i0, i1, sh);
-    for (int r = warp; r < k.nrows; r += kWarps) {
+    int it = 0;
+    if (warp == kWarps) {
+        attn_feed<DP, Q4, NT>(p, maps, k, kvh, i0, i1, sh, ring, &it);
+        feed_end<R::kStages>(sh, it);
+    } else
+        attn_piece<DP, NT, Q4>(p, k, kvh, i0, i1, sh, ring, &it);
+    for (int r = warp; warp < kWarps && r < k.nrows; r += kWarps) {
         float m, l, acc[E];
         attn_piece_row<DP, NT, Q4>(p, k, kvh, i0, i1, sh, r, &m, &l, acc);
         if (size == 1) {
@@ -667,11 +769,13 @@ attn_cluster_kernel(const __grid_constant__ AttnParams p)
             sh.l[0][r] = l;
         }
     }
+    if (warp == 0 && lane == 0 && sh.abort)
+        atomicOr(p.status, kStatusWait);
     if (size == 1)
         return;
     cluster.sync();
     // rows go round the cluster's warps; parts are added in rank order
-    for (int r = rank * kWarps + warp; r < k.nrows; r += size * kWarps) {
+    for (int r = rank * kWarps + warp; warp < kWarps && r < k.nrows; r += size * kWarps) {
         float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e)
@@ -698,11 +802,19 @@ constexpr int kPieceCost = 8;
 
 // Much work: every CTA takes the same number of tiles, kPieceCost more a block.
 template <int DP, int NT, bool Q4>
-__global__ void __launch_bounds__(32 * kWarps, rows_ctas(DP, NT, Q4))
-attn_rows_kernel(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(kThreads, Rows<DP, Q4, NT>::kCtas)
+attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CacheMaps maps)
 {
     constexpr int E = DP / 32;
-    __shared__ __align__(16) RowsShared<DP, NT> sh;
+    using R = Rows<DP, Q4, NT>;
+    extern __shared__ __align__(1024) uint8_t ring[];
+    auto &sh = *reinterpret_cast<RowsShared<DP, NT> *>(ring + R::kStages * R::kStageBytes);
+    if (sm_u32(ring) & 1023u) {     // the copies' swizzle counts on it
+        if (threadIdx.x == 0)
+            atomicOr(p.status, kStatusWait);
+        return;
+    }
+    rows_setup<DP, NT>(sh, Q4 && !p.dense_scales ? 33 : 1);
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -732,7 +844,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p)
         __syncthreads();
         int add = 0, all = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < kWarps + 1; ++w) {
             add += w < warp ? sh.scan[w] : 0;
             all += sh.scan[w];
         }
@@ -741,7 +853,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p)
     };
     int64_t all_tiles = 0;
     int mine = 0, upto = 0;        // of the chunk of sequences looked at last
-    for (int b0 = 0; b0 < p.B; b0 += 32 * kWarps) {
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
         int total;
         mine = tiles_of(b0 + threadIdx.x);
         upto = scan(mine, &total);
@@ -761,9 +873,9 @@ attn_rows_kernel(const __grid_constant__ AttnParams p)
     // the sequence `at` falls in
     int64_t before = 0;
     int b = -1;
-    for (int b0 = 0; b < 0; b0 += 32 * kWarps) {
+    for (int b0 = 0; b < 0; b0 += kThreads) {
         int total;
-        if (p.B > 32 * kWarps) {
+        if (p.B > kThreads) {
             mine = tiles_of(b0 + threadIdx.x);
             upto = scan(mine, &total);
         } else {
@@ -784,6 +896,10 @@ attn_rows_kernel(const __grid_constant__ AttnParams p)
         }
     }
 
+    // The feeding warp and the computing ones walk the same pieces, each at its
+    // own pace.
+    const bool feeds = warp == kWarps;
+    int it = 0;
     bool first = true;
     while (at < end) {
         // the next sequence with rows of this launch
@@ -803,11 +919,15 @@ attn_rows_kernel(const __grid_constant__ AttnParams p)
             at += to - from;
             if (i0 == i1)
                 continue;        // the share ends before the block's first tile
-            __syncthreads();     // sh is free
+            if (feeds) {
+                attn_feed<DP, Q4, NT>(p, maps, k, kvh, i0, min(i1, k.ntiles), sh, ring, &it);
+                continue;
+            }
+            compute_sync();      // the last piece has been written out
             if (threadIdx.x == 0)
                 sh.poison = 0;
-            __syncthreads();
-            attn_piece<DP, NT, Q4>(p, k, kvh, i0, min(i1, k.ntiles), sh);
+            compute_sync();
+            attn_piece<DP, NT, Q4>(p, k, kvh, i0, min(i1, k.ntiles), sh, ring, &it);
             const bool only = i0 == 0 && i1 == tiles;
             const int slot = 2 * (int)blockIdx.x + (first ? 0 : 1);
             for (int r = warp; r < k.nrows; r += kWarps) {
@@ -845,7 +965,10 @@ attn_rows_kernel(const __grid_constant__ AttnParams p)
             before += cost;
             ++b;
         }
-    }
+    }    if (feeds)
+        feed_end<R::kStages>(sh, it);
+    else if (threadIdx.x == 0 && sh.abort)
+        atomicOr(p.status, kStatusWait);
 }
 
 // Joins the pieces of the block that CTA x / rows began, row x % rows.
@@ -991,19 +1114,22 @@ __global__ void __launch_bounds__(32 * kWarps) attn_join_kernel(const __grid_con
 template <int DP, int NT, bool Q4>
 cudaError_t rows_launch(const AttnParams &p, cudaStream_t stream, LaunchRecord *rec)
 {
-    const dim3 block(32 * kWarps);
-    if (p.ctas == 0) {
-        rec->grid = p.n_blocks * p.c.Hkv * p.cluster;
-        rec->cluster = p.cluster;
-        return launch(attn_cluster_kernel<DP, NT, Q4>, dim3((unsigned)rec->grid), block, 0, stream,
-                      p.cluster, p);
-    }
-    rec->grid = p.ctas;
-    cudaError_t e = launch(attn_rows_kernel<DP, NT, Q4>, dim3((unsigned)p.ctas), block, 0, stream, 1,
-                           p);
-    if (e == cudaSuccess) {
-        e = launch(attn_rows_join_kernel<DP>, dim3((unsigned)(p.ctas * p.rows)), block, 0, stream, 1,
-                   p);
+    using R = Rows<DP, Q4, NT>;
+    constexpr int smem = R::kStages * R::kStageBytes + (int)sizeof(RowsShared<DP, NT>);
+    CacheMaps maps;
+    auto fn = p.ctas ? attn_rows_kernel<DP, NT, Q4> : attn_cluster_kernel<DP, NT, Q4>;
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(fn), smem);
+    if (e == cudaSuccess)
+        e = cache_maps(p.c, Q4, 16, &maps);
+    if (e != cudaSuccess)
+        return e;
+    rec->grid = p.ctas ? p.ctas : p.n_blocks * p.c.Hkv * p.cluster;
+    rec->cluster = p.ctas ? 1 : p.cluster;
+    e = launch(fn, dim3((unsigned)rec->grid), dim3(kThreads), smem, stream, rec->cluster, p,
+               maps);
+    if (e == cudaSuccess && p.ctas) {
+        e = launch(attn_rows_join_kernel<DP>, dim3((unsigned)(p.ctas * p.rows)), dim3(32 * kWarps), 0,
+                   stream, 1, p);
         rec->launches += 1;
     }
     return e;
@@ -1013,7 +1139,11 @@ cudaError_t rows_launch(const AttnParams &p, cudaStream_t stream, LaunchRecord *
 
 int attn_rows_resident(int64_t D, int rows, int q4)
 {
-    return rows_ctas(D <= 64 ? 64 : 128, rows == 8 ? 1 : 2, q4 != 0);
+    if (D <= 64)
+        return rows == 8 ? (q4 ? Rows<64, true, 1>::kCtas : Rows<64, false, 1>::kCtas)
+                         : (q4 ? Rows<64, true, 2>::kCtas : Rows<64, false, 2>::kCtas);
+    return rows == 8 ? (q4 ? Rows<128, true, 1>::kCtas : Rows<128, false, 1>::kCtas)
+                     : (q4 ? Rows<128, true, 2>::kCtas : Rows<128, false, 2>::kCtas);
 }
 
 cudaError_t launch_attn_rows(const AttnParams &p, int q4, cudaStream_t stream, LaunchRecord *rec)
@@ -1031,7 +1161,7 @@ cudaError_t launch_attn_rows(const AttnParams &p, int q4, cudaStream_t stream, L
                               : rows_launch<128, 2, false>(p, stream, rec));
     if (e == cudaSuccess) {
         rec->kernel = QKR_KERNEL_ATTN_ROWS;
-        rec->block = 32 * kWarps;
+        rec->block = kThreads;
         rec->stages = p.ctas ? p.ctas : p.cluster;
         rec->heads_per_item = p.rows;
         rec->launches += 1;

@@ -42,9 +42,8 @@
 // all roles stop issuing, copies and matrix instructions in flight are waited
 // for (bounded), tensor memory is freed and the block ends.
 
-#include <cuda.h>
-
 #include "cache_attn.cuh"
+#include "cache_tma.cuh"
 
 namespace qkr {
 namespace {
@@ -187,24 +186,6 @@ __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.al
 template <int REGS>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS)); }
 
-// The tensor map's coordinates for (row, head, page): its axes are in the
-// order of their strides.
-struct TileMap {
-    CUtensorMap k, v;
-    int axis_row_k, axis_head_k, axis_page_k;  // 1..3
-    int axis_row_v, axis_head_v, axis_page_v;
-    int box;                                   // keys of one copy: divides the tile and the page
-};
-
-__device__ __forceinline__ void tma_load(const CUtensorMap *m, uint32_t dst, uint64_t *bar, int x,
-                                         int c1, int c2, int c3)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-        "[%1, {%3, %4, %5, %6}], [%2];"
-        ::"r"(dst), "l"(m), "r"(smem_u32(bar)), "r"(x), "r"(c1), "r"(c2), "r"(c3) : "memory");
-}
-
 // Order of the eight elements of a 16-byte chunk of a 4-bit row in shared
 // memory: 0 4 1 5 2 6 3 7, as the nibbles pair up.  Q's chunks follow it for
 // the first product, O's columns are read back through it.
@@ -216,7 +197,7 @@ __device__ __forceinline__ uint4 pair_order(const uint4 &v)
 
 template <int DP, bool Q4>
 __global__ void __launch_bounds__(Q4 ? 512 : 384, 1)
-attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ TileMap map)
+attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CacheMaps map)
 {
     using Lay = Layout<DP>;
     constexpr int NST = Lay::kStages;
@@ -500,12 +481,12 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         // ================================================ TMA
         // A lane owns one copy of a tile: `box` keys, 64 dims.  It looks its page
         // up once for K and V and asks for the next tile's before it waits.
-        const int copies = kTile / map.box * Lay::kHalves;
-        const int hf = lane % Lay::kHalves, c = lane / Lay::kHalves * map.box;
+        const int copies = kTile / map.k.box * Lay::kHalves;
+        const int hf = lane % Lay::kHalves, c = lane / Lay::kHalves * map.k.box;
         const bool mine = lane < copies;
         auto look = [&](int j, int *page, int *row) {
             // a copy no row sees any key of reads zeros: a page past the last
-            const int a = k.tile_at(i0 + j) * kTile + c, z = a + map.box;
+            const int a = k.tile_at(i0 + j) * kTile + c, z = a + map.k.box;
             *page = -1;
             if (mine && j < nt && ((a < k.hi && z > k.lo) || a < k.sink))
                 *page = attn_page(p, k.b, a, hf == 0);
@@ -534,13 +515,9 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                 bar_expect(bar, Lay::kStageBytes);
             __syncwarp();
             if (mine) {
-                const int ar = is_v ? map.axis_row_v : map.axis_row_k;
-                const int ah = is_v ? map.axis_head_v : map.axis_head_k;
-                tma_load(is_v ? &map.v : &map.k,
-                         smem_u32(ring + st * Lay::kStageBytes + hf * kTile * 128) + c * 128, bar,
-                         64 * hf, ar == 1 ? row : (ah == 1 ? kvh : page),
-                         ar == 2 ? row : (ah == 2 ? kvh : page),
-                         ar == 3 ? row : (ah == 3 ? kvh : page));
+                plane_load(is_v ? map.v : map.k,
+                           smem_u32(ring + st * Lay::kStageBytes + hf * kTile * 128) + c * 128,
+                           smem_u32(bar), 64 * hf, row, kvh, page);
             }
             if (is_v) {
                 page = page_next;
@@ -701,74 +678,11 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         atomicOr(p.status, kStatusWait);
 }
 
-// The driver's tensor-map encoder, without linking the driver library.
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-cudaError_t encoder(EncodeFn *fn)
-{
-    static EncodeFn found = nullptr;   // the same address for every caller
-    if (!found) {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult res;
-        cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
-                                                         cudaEnableDefault, &res);
-        if (e != cudaSuccess)
-            return e;
-        if (res != cudaDriverEntryPointSuccess || !f)
-            return cudaErrorNotSupported;
-        found = reinterpret_cast<EncodeFn>(f);
-    }
-    *fn = found;
-    return cudaSuccess;
-}
-
-cudaError_t encode(const CacheView &c, const CachePlane &pl, int box, CUtensorMap *m, int *axis_row,
-                   int *axis_head, int *axis_page)
-{
-    EncodeFn fn;
-    cudaError_t e = encoder(&fn);
-    if (e != cudaSuccess)
-        return e;
-    // axes by stride; the stride of an axis of one is free, so it goes last
-    struct Axis {
-        int64_t stride, extent;
-        int box, *at;
-    } ax[3] = {{pl.rs, c.page_size, box, axis_row},
-               {pl.hs, c.Hkv, 1, axis_head},
-               {pl.ps, c.n_pages, 1, axis_page}};
-    for (Axis &a : ax)
-        if (a.extent == 1)
-            a.stride = (int64_t)1 << 39;
-    for (int i = 0; i < 2; ++i)
-        for (int j = 0; j < 2 - i; ++j)
-            if (ax[j].stride > ax[j + 1].stride) {
-                const Axis t = ax[j];
-                ax[j] = ax[j + 1];
-                ax[j + 1] = t;
-            }
-    cuuint64_t dims[4] = {(cuuint64_t)c.D, 0, 0, 0}, strides[3];
-    cuuint32_t boxes[4] = {64, 0, 0, 0}, steps[4] = {1, 1, 1, 1};
-    for (int i = 0; i < 3; ++i) {
-        dims[i + 1] = (cuuint64_t)ax[i].extent;
-        strides[i] = (cuuint64_t)ax[i].stride;
-        boxes[i + 1] = (cuuint32_t)ax[i].box;
-        *ax[i].at = i + 1;
-    }
-    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pl.base, dims, strides, boxes, steps,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <int DP, bool Q4>
-cudaError_t tiles_launch(const AttnParams &p, const TileMap &map, cudaStream_t stream)
+cudaError_t tiles_launch(const AttnParams &p, const CacheMaps &map, cudaStream_t stream)
 {
     auto fn = attn_tiles_kernel<DP, Q4>;
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Layout<DP>::kBytes);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(fn), Layout<DP>::kBytes);
     if (e != cudaSuccess)
         return e;
     const dim3 grid((unsigned)(p.n_blocks * p.c.Hkv * p.nsplit));
@@ -779,18 +693,10 @@ cudaError_t tiles_launch(const AttnParams &p, const TileMap &map, cudaStream_t s
 
 cudaError_t launch_attn_tiles(const AttnParams &p, int q4, cudaStream_t stream, LaunchRecord *rec)
 {
-    TileMap map = {};
+    CacheMaps map = {};
     cudaError_t e = cudaSuccess;
-    if (!q4) {
-        map.box = kTile;
-        while (p.c.page_size % map.box)
-            map.box /= 2;
-        e = encode(p.c, p.c.k, map.box, &map.k, &map.axis_row_k, &map.axis_head_k,
-                   &map.axis_page_k);
-        if (e == cudaSuccess)
-            e = encode(p.c, p.c.v, map.box, &map.v, &map.axis_row_v, &map.axis_head_v,
-                       &map.axis_page_v);
-    }
+    if (!q4)
+        e = cache_maps(p.c, false, kTile, &map);
     if (e == cudaSuccess) {
         if (p.c.D <= 64)
             e = q4 ? tiles_launch<64, true>(p, map, stream) : tiles_launch<64, false>(p, map, stream);

@@ -64,6 +64,7 @@ struct AttnParams {
     float *ws_o;
     float2 *ws_ml;
     struct AttnSpan *ws_span;
+    int dense_scales;        // 4 bits: the scale rows of a page and head are one run, on 16 bytes
     unsigned *status;
 };
 
@@ -271,6 +272,10 @@ __device__ __forceinline__ void attn_emit(const AttnParams &p, const AttnBlock &
 
 // CTAs of the even-shares rows kernel an SM holds.
 int attn_rows_resident(int64_t D, int rows, int q4);
+
+// Lets a kernel have `bytes` of dynamic shared memory on the current device;
+// asked of the driver once for each kernel and device.
+cudaError_t allow_smem(const void *fn, int bytes);
 
 // Launchers.
 cudaError_t launch_attn_rows(const AttnParams &p, int q4, cudaStream_t stream, LaunchRecord *rec);
