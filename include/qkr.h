@@ -472,7 +472,8 @@ qkr_status cache_attention(void *stream, const qkr_cache_desc *cache, const void
                            int64_t workspace_bytes);
 
 /* Bytes of workspace a cache_attention call of these sizes needs on the
- * current device (0: none).  Of the cache only format, Hkv and D are read. */
+ * current device (0: none).  Of the cache only format, page_size, Hkv and D are
+ * read. */
 qkr_status cache_attention_workspace(const qkr_cache_desc *cache, int64_t T, int64_t Hq,
                                      int64_t B, int64_t max_q, int64_t max_len, int64_t window,
                                      int64_t n_sink, int64_t *bytes);

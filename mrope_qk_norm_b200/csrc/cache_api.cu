@@ -258,7 +258,7 @@ void cut(const Sizes &s, int64_t tiles, int64_t split, qkr::AttnParams *p, int64
 // as many new tokens as every sequence having max_q would make, is one kind.
 constexpr int64_t kFewRows = 16;
 
-qkr_status make_plan(const Sizes &s, Plan *plan)
+qkr_status make_plan(const Sizes &s, int64_t page_size, Plan *plan)
 {
     int sms = 0;
     qkr_status st = current_device(&sms, &plan->status);
@@ -270,26 +270,34 @@ qkr_status make_plan(const Sizes &s, Plan *plan)
     if (plan->rows) {
         qkr::AttnParams &p = plan->pr;
         const int64_t cap = plan->tiles ? kFewRows : INT_MAX;
-        const int64_t tiles = blocks(s, (most < cap ? most : cap) <= 8 ? 8 : 16, 16, 0, cap, &p);
+        int shift = 6;
+        while (page_size % ((int64_t)1 << shift))
+            --shift;
+        p.tile_shift = shift;
+        const int64_t tiles = blocks(s, (most < cap ? most : cap) <= 8 ? 8 : 16, 1 << shift, 0, cap, &p);
+        const int64_t keys = tiles << shift;
         const int64_t items = p.n_blocks * s.Hkv;   // one block a sequence
         const int64_t slots = (int64_t)sms * qkr::attn_rows_resident(s.D, p.rows, s.q4);
-        // A cluster a block, as large as leaves a warp two tiles and the clusters
-        // room, where a warp then has at most 6 tiles.  Else even shares, of no
-        // less than 8 tiles.
+        // A cluster a block, as large as leaves a warp 32 keys and the clusters
+        // room, where a warp then has at most 96 keys.  Else even shares, of no
+        // less than 128 keys; a block counts for 128 keys more (8192-key decode
+        // batch: 88 us at 0, 72 at 128).
         p.nsplit = 1;
         int64_t size = 1;
-        while (size < 8 && tiles > size * 8 && items * size * 2 <= slots)
+        while (size < 8 && keys > size * 128 && items * size * 2 <= slots)
             size *= 2;
-        if (tiles <= size * 4 * 6 && items * size <= 2 * slots) {
+        if (keys <= size * 4 * 96 && items * size <= 2 * slots) {
             p.cluster = (int)size;
         } else {
             p.ctas = (int)slots;
-            p.split_tiles = 8;
+            p.split_tiles = 128 >> shift;
+            p.piece_cost = 128 >> shift;
             plan->ws_bytes = slots * (2 * p.rows * (s.D + 2) * 4 + (int64_t)sizeof(qkr::AttnSpan));
         }
     }
     if (plan->tiles) {
         qkr::AttnParams &p = plan->pt;
+        p.tile_shift = 7;
         const int64_t tiles = blocks(s, 256, 128, plan->rows ? kFewRows : 0, INT_MAX, &p);
         // A block's keys are cut only where the blocks alone do not fill the
         // SMs: a part costs 256 partial rows written and read again.
@@ -336,8 +344,11 @@ qkr_status cache_attention_workspace(const qkr_cache_desc *cache, int64_t T, int
                cache->format == QKR_CACHE_Q4};
     if ((st = check_sizes(s)) != QKR_OK)
         return st;
+    if (cache->page_size < 16 || cache->page_size > 65536 || cache->page_size % 16)
+        return api_fail(QKR_ERR_UNSUPPORTED, "page_size %d: need a multiple of 16 in [16, 65536]",
+                        cache->page_size);
     Plan plan;
-    if (s.T && s.B && s.max_q && (st = make_plan(s, &plan)) != QKR_OK)
+    if (s.T && s.B && s.max_q && (st = make_plan(s, cache->page_size, &plan)) != QKR_OK)
         return st;
     *bytes = plan.ws_bytes;
     return api_done(qkr::LaunchRecord());
@@ -391,7 +402,7 @@ qkr_status cache_attention(void *stream, const qkr_cache_desc *cache, const void
     if ((st = check_overlap(written, read, view, q4)) != QKR_OK)
         return st;
     Plan plan;
-    if ((st = make_plan(s, &plan)) != QKR_OK)
+    if ((st = make_plan(s, view.page_size, &plan)) != QKR_OK)
         return st;
     if (plan.ws_bytes > 0) {
         if (!workspace || workspace_bytes < plan.ws_bytes)
@@ -440,8 +451,9 @@ qkr_status cache_attention(void *stream, const qkr_cache_desc *cache, const void
                 if (pl->rs != s.D / 16 || pl->hs % 16 || pl->ps % 16 || !aligned(pl->base, 16))
                     p.dense_scales = 0;
         }
-        const uint64_t page_tiles = view.page_size / 16;
-        p.page_recip = (((uint64_t)1 << 38) + page_tiles - 1) / page_tiles;
+        const uint64_t page_tiles = view.page_size >> p.tile_shift;
+        if (!which)
+            p.page_recip = (((uint64_t)1 << 38) + page_tiles - 1) / page_tiles;
         p.status = plan.status;
         const cudaStream_t cs = static_cast<cudaStream_t>(stream);
         if (which && p.scale_log2 == 0.f)

@@ -18,7 +18,12 @@ __device__ __forceinline__ uint32_t sub136(uint32_t x)
 // Nibbles i and i + 4 of w as the bf16 pair (128 + n_i, 128 + n_{i+4}).
 __device__ __forceinline__ uint32_t nibbles(uint32_t w, int i)
 {
-    return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    // one three-input instruction: with both constants written as immediates the
+    // compiler makes two of it
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;"
+        : "=r"(r) : "r"(w >> (4 * i)), "r"(0x000f000fu), "r"(0x43004300u));
+    return r;
 }
 
 __device__ __forceinline__ bool nonfinite2(uint32_t w)  // either bf16 of the word

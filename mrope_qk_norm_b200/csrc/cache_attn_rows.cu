@@ -16,8 +16,9 @@
 // One warp feeds, four compute.  The feeding warp looks the pages up and copies
 // rows by TMA into a ring in shared memory, up to 96 KB ahead; the ring runs on
 // from block to block, so a short sequence costs no pause.  A stage holds a step
-// of every computing warp: one tile of 16 keys in bf16, two in 4 bits (18 KB).
-// Which key of a tile is which row of the operand is free as well; the order
+// of every computing warp: 16 keys in bf16, 32 in 4 bits (18 KB).  A tile is what
+// one copy takes: 64 keys, or 32 or 16 where the page is not a multiple of that.
+// Which of 16 keys is which row of the operand is free as well; the order
 // below makes the operand loads of eight lanes meet eight different banks in
 // the layout the copies leave.  Where a scale row is not one of a dense run,
 // its 8 (4) bytes come by cp.async.  Before this the warps loaded their own
@@ -115,7 +116,7 @@ struct alignas(16) RowsShared {
     uint64_t full[4], empty[4];
 };
 
-// The key of a tile that is row `r` of the operand, and where 16-byte chunk `ch`
+// Which of 16 keys is row `r` of the operand, and where 16-byte chunk `ch`
 // of key t of the stage lies from the start of its K or V part.
 template <int DP, bool Q4>
 __device__ __forceinline__ int key_of(int r)
@@ -219,9 +220,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 }
 
 // The feeding warp: tiles [i0, i1) of a block and KV head into the ring, which
-// stands at its stage number `it`.  A lane owns one copy of a stage: the 16 keys
-// of a tile (always within one page), of K or V, 64 dims (bf16) or the codes or
-// the scales (4 bits).
+// stands at its stage number `it`.  A lane owns one copy of a stage: a tile of
+// K or V, 64 dims (bf16) or the codes or the scales (4 bits).
 template <int DP, bool Q4, int NT>
 __device__ __forceinline__ void attn_feed(const AttnParams &p, const CacheMaps &maps,
                                           const AttnBlock &k, int kvh, int i0, int i1,
@@ -230,7 +230,7 @@ __device__ __forceinline__ void attn_feed(const AttnParams &p, const CacheMaps &
     using R = Rows<DP, Q4, NT>;
     constexpr int KINDS = Q4 ? 4 : 2 * R::kHalves;
     const int lane = threadIdx.x & 31;
-    constexpr int box = 16;
+    const int box = p.tile, step = R::kKeys >> p.tile_shift;
     const int kind = lane % KINDS, first = lane / KINDS * box;
     const bool mine = first < R::kKeys;
     const bool is_v = Q4 ? kind & 1 : kind >= R::kHalves;
@@ -247,23 +247,23 @@ __device__ __forceinline__ void attn_feed(const AttnParams &p, const CacheMaps &
     auto look = [&](int i, int *page, int *row) {
         *page = -2;
         *row = 0;
-        i += first / 16;
+        i += first >> p.tile_shift;
         if (!mine || i >= i1)
             return;
         const int at = k.tile_at(i);
         // division by the tiles of a page: exact for tiles below 2^26
         const int pg = (int)((uint64_t)at * p.page_recip >> 38);
-        *row = at * 16 - pg * p.c.page_size;
+        *row = (at << p.tile_shift) - pg * p.c.page_size;
         *page = table[pg];
     };
     int page, row;
     look(i0, &page, &row);
-    for (int i = i0; i < i1; i += R::kKeys / 16, ++*it) {
+    for (int i = i0; i < i1; i += step, ++*it) {
         const int st = *it % R::kStages;
         const uint32_t at = sm_u32(ring) + st * R::kStageBytes + to;
         const uint32_t bar = sm_u32(&sh.full[st]);
         int page_next, row_next;
-        look(i + R::kKeys / 16, &page_next, &row_next);
+        look(i + step, &page_next, &row_next);
         if (page != -2 && (unsigned)page >= (unsigned)p.c.n_pages) {
             atomicOr(p.status, kStatusBounds);
             page = -1;
@@ -296,9 +296,9 @@ __device__ __forceinline__ void attn_feed(const AttnParams &p, const CacheMaps &
             if (!p.dense_scales) {
                 // one row a lane and step, K and V in turn
                 for (int x = lane; x < 2 * R::kKeys; x += 32) {
-                    const int t = x % R::kKeys, own = t / box * KINDS + 2 + x / R::kKeys;
+                    const int t = x % R::kKeys, own = (t >> p.tile_shift) * KINDS + 2 + x / R::kKeys;
                     const int pg = __shfl_sync(0xffffffffu, page, own);
-                    const int rw = __shfl_sync(0xffffffffu, row, own) + t % box;
+                    const int rw = __shfl_sync(0xffffffffu, row, own) + (t & (box - 1));
                     const CachePlane &pl = x < R::kKeys ? p.c.ks : p.c.vs;
                     const uint8_t *src = pl.base + kvh * pl.hs +
                                          (pg < 0 ? 0 : (uint64_t)pg * (uint32_t)pl.ps +
@@ -402,20 +402,27 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
     }
     bool poison = false;
     // Tiles [in0, in1) of the piece: every row sees all their keys.
-    const int in0 = k.c_sink +
-                    (p.window ? max(0, (max(0, k.p_last - p.window + 1) + 15) / 16 - k.c0) : 0);
-    const int in1 = min(i1, k.c_sink + (k.p_first + 1) / 16 - k.c0);
+    const int sh_t = p.tile_shift;
+    const int in0 =
+        k.c_sink +
+        (p.window ? max(0, ((max(0, k.p_last - p.window + 1) + p.tile - 1) >> sh_t) - k.c0) : 0);
+    const int in1 = min(i1, k.c_sink + ((k.p_first + 1) >> sh_t) - k.c0);
+    const int t0 = warp * U * 16;           // the warp's first key of a stage
+    const int step = R::kKeys >> sh_t;      // tiles of a stage
+    auto key_at = [&](int i, int t) {       // the token that is key t of the stage at tile i
+        i += t >> sh_t;
+        return i < i1 ? (k.tile_at(i) << sh_t) + (t & (p.tile - 1)) : INT_MAX / 2;
+    };
     constexpr int KEYS = R::kKeys;
     const int gk = key_of<DP, Q4>(g);       // the lane's keys: gk, gk + 8 of K and S ...
     const int vk[2] = {key_of<DP, Q4>(2 * c), key_of<DP, Q4>(2 * c + 1)};   // ... these, + 8 of V
 
-    for (int i = i0 + warp * U; i - warp * U < i1; i += kWarps * U, ++*it) {
+    for (int i = i0; i < i1; i += step, ++*it) {
         const int st = *it % R::kStages;
         bar_wait(&sh.full[st], (*it / R::kStages) & 1, &sh.abort);
-        if (i < i1) {
+        if (i + (t0 >> sh_t) < i1) {
         const uint8_t *stage = ring + st * R::kStageBytes;
-        const int t0 = warp * U * 16;           // the warp's first key of the stage
-        const bool full = i >= in0 && i + U <= in1;
+        const bool full = i + (t0 >> sh_t) >= in0 && i + ((t0 + 16 * U - 1) >> sh_t) < in1;
 
         // S^T: lane has keys g, g + 8 (elements 0 and 1, 2 and 3) of columns 2c, 2c + 1
         float s[U][NT][4];
@@ -481,7 +488,7 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
         if (!full) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int j0 = i + u < i1 ? k.tile_at(i + u) * 16 : INT_MAX / 2;
+                const int j0 = key_at(i, t0 + 16 * u);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -541,10 +548,10 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             // the second of two tiles may lie beyond the piece: nothing was copied there
-            if (u && i + u >= i1)
+            if (u && i + ((t0 + 16 * u) >> sh_t) >= i1)
                 break;
             const uint8_t *vpart = stage + R::kPart;
-            const int tk = t0 + 16 * u, j0 = full ? 0 : k.tile_at(i + u) * 16;
+            const int tk = t0 + 16 * u, j0 = full ? 0 : key_at(i, tk);
             if constexpr (Q4) {
                 uint32_t vw[4][GR / 2], vs[2][GR / 2];
 #pragma unroll
@@ -796,11 +803,8 @@ attn_cluster_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     cluster.sync();     // nobody leaves while its memory is read
 }
 
-// What a piece costs beside its tiles (the first loads' latency, the warps'
-// join), in tiles: counted at the front of every block's share.
-constexpr int kPieceCost = 8;
-
-// Much work: every CTA takes the same number of tiles, kPieceCost more a block.
+// Much work: every CTA takes the same number of tiles, a block counting for
+// p.piece_cost more at its front (the first loads' latency, the warps' join).
 template <int DP, int NT, bool Q4>
 __global__ void __launch_bounds__(kThreads, Rows<DP, Q4, NT>::kCtas)
 attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CacheMaps maps)
@@ -827,7 +831,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
         bool bad;
         const int n = attn_seq(p, b, &t0, &bad);
         return attn_blocks_of(p, n)
-                   ? kPieceCost + max(1, attn_block_at(p, b, 0, n, t0, bad).ntiles)
+                   ? p.piece_cost + max(1, attn_block_at(p, b, 0, n, t0, bad).ntiles)
                    : 0;
     };
     // inclusive sum over the CTA's threads, and the total
@@ -909,12 +913,12 @@ attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
         while (!attn_blocks_of(p, n))
             n = attn_seq(p, ++b, &t0, &bad);
         const AttnBlock k = attn_block_at(p, b, 0, n, t0, bad);
-        const int tiles = max(1, k.ntiles), cost = kPieceCost + tiles;
+        const int tiles = max(1, k.ntiles), cost = p.piece_cost + tiles;
         const int64_t off = at - before * Hkv;
         int kvh = (int)(off / cost), from = (int)(off % cost);
         for (; kvh < Hkv && at < end; ++kvh, from = 0) {
             const int to = (int)min((int64_t)cost, from + end - at);
-            const int i0 = max(0, from - kPieceCost), i1 = max(0, to - kPieceCost);
+            const int i0 = max(0, from - p.piece_cost), i1 = max(0, to - p.piece_cost);
             const int64_t last = at - from + cost - 1;   // the block's last unit
             at += to - from;
             if (i0 == i1)
@@ -1120,7 +1124,7 @@ cudaError_t rows_launch(const AttnParams &p, cudaStream_t stream, LaunchRecord *
     auto fn = p.ctas ? attn_rows_kernel<DP, NT, Q4> : attn_cluster_kernel<DP, NT, Q4>;
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(fn), smem);
     if (e == cudaSuccess)
-        e = cache_maps(p.c, Q4, 16, &maps);
+        e = cache_maps(p.c, Q4, p.tile, &maps);
     if (e != cudaSuccess)
         return e;
     rec->grid = p.ctas ? p.ctas : p.n_blocks * p.c.Hkv * p.cluster;

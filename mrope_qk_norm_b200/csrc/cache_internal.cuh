@@ -51,10 +51,12 @@ struct AttnParams {
     int blocks_max;          // blocks a sequence can have (max_q*G over rows)
     int direct;              // 1: block index = b*blocks_max + block; 0: blocks counted from cu
     int64_t n_blocks;        // block indices of the grid
-    int tile;                // keys of a tile: 16 or 128
+    int tile;                // keys of a tile: 16, 32 or 64 (rows kernel), 128
+    int tile_shift;          // its logarithm
+    int piece_cost;          // rows kernel: what a block counts for beside its tiles
     int split_tiles;         // tiles of a part of a block's keys
     int nsplit;              // parts at most
-    uint64_t page_recip;     // rows kernel: ceil(2^38 / (tiles of a page))
+    uint64_t page_recip;     // rows kernel: ceil(2^38 / tiles of a page)
     int ctas;                // rows kernel: CTAs that share all keys evenly; 0: a cluster a block
     int cluster;             // CTAs of such a cluster
     // Partial outputs (not divided by l), their maxima (log2 units) and sums.
