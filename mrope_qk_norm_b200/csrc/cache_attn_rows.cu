@@ -127,6 +127,7 @@ __device__ __forceinline__ int key_of(int r)
                                                 : 0x67453210u); // 0 1 2 3 5 4 7 6
     return (r & 8) + (int)(order >> (4 * (r & 7)) & 7u);
 }
+// (Adding a multiple of 8 to t adds that many rows: the turning has period 8.)
 template <int DP, bool Q4, int KEYS>
 __device__ __forceinline__ int chunk_at(int t, int ch)
 {
@@ -177,7 +178,7 @@ __device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity)
 }
 // Bounded; after a wait that ran out no other waits (the result is reported as
 // not valid, nothing is accessed that would not be otherwise).
-__device__ __forceinline__ void bar_wait(uint64_t *bar, uint32_t parity, int *abort)
+__device__ __noinline__ void bar_wait_long(uint64_t *bar, uint32_t parity, int *abort)
 {
     for (uint32_t i = 0; i < kWaitLimit; ++i) {
         if (bar_try(bar, parity))
@@ -187,6 +188,26 @@ __device__ __forceinline__ void bar_wait(uint64_t *bar, uint32_t parity, int *ab
     }
     *reinterpret_cast<volatile int *>(abort) = 1;
 }
+__device__ __forceinline__ void bar_wait(uint64_t *bar, uint32_t parity, int *abort)
+{
+    if (!__all_sync(0xffffffffu, bar_try(bar, parity)))
+        bar_wait_long(bar, parity, abort);
+}
+
+// A warp's place in the ring.
+template <int STAGES>
+struct RingAt {
+    int st = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++st == STAGES) {
+            st = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
 // The computing warps among themselves.
 __device__ __forceinline__ void compute_sync()
 {
@@ -219,13 +240,14 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
         ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
-// The feeding warp: tiles [i0, i1) of a block and KV head into the ring, which
-// stands at its stage number `it`.  A lane owns one copy of a stage: a tile of
+// The feeding warp: tiles [i0, i1) of a block and KV head into the ring from
+// `at` on.  A lane owns one copy of a stage: a tile of
 // K or V, 64 dims (bf16) or the codes or the scales (4 bits).
 template <int DP, bool Q4, int NT>
 __device__ __forceinline__ void attn_feed(const AttnParams &p, const CacheMaps &maps,
                                           const AttnBlock &k, int kvh, int i0, int i1,
-                                          RowsShared<DP, NT> &sh, uint8_t *ring, int *it)
+                                          RowsShared<DP, NT> &sh, uint8_t *ring,
+                                          RingAt<Rows<DP, Q4, NT>::kStages> *at)
 {
     using R = Rows<DP, Q4, NT>;
     constexpr int KINDS = Q4 ? 4 : 2 * R::kHalves;
@@ -258,9 +280,9 @@ __device__ __forceinline__ void attn_feed(const AttnParams &p, const CacheMaps &
     };
     int page, row;
     look(i0, &page, &row);
-    for (int i = i0; i < i1; i += step, ++*it) {
-        const int st = *it % R::kStages;
-        const uint32_t at = sm_u32(ring) + st * R::kStageBytes + to;
+    for (int i = i0; i < i1; i += step, at->next()) {
+        const int st = at->st;
+        const uint32_t dst = sm_u32(ring) + st * R::kStageBytes + to;
         const uint32_t bar = sm_u32(&sh.full[st]);
         int page_next, row_next;
         look(i + step, &page_next, &row_next);
@@ -268,8 +290,8 @@ __device__ __forceinline__ void attn_feed(const AttnParams &p, const CacheMaps &
             atomicOr(p.status, kStatusBounds);
             page = -1;
         }
-        if (*it >= R::kStages)
-            bar_wait(&sh.empty[st], (*it / R::kStages - 1) & 1, &sh.abort);
+        // (the stages' first use finds the phase before the first complete)
+        bar_wait(&sh.empty[st], at->phase ^ 1u, &sh.abort);
         __syncwarp();
         const bool by_bulk = !scales || p.dense_scales;
         const bool copies = page >= 0 || (page == -1 && !scales);
@@ -286,10 +308,10 @@ __device__ __forceinline__ void attn_feed(const AttnParams &p, const CacheMaps &
         __syncwarp();
         if (issue) {
             if (scales)
-                bulk_load(at, sp.base + kvh * sp.hs + (uint64_t)page * (uint32_t)sp.ps +
+                bulk_load(dst, sp.base + kvh * sp.hs + (uint64_t)page * (uint32_t)sp.ps +
                                   (uint64_t)(uint32_t)row * (uint32_t)sp.rs, bytes, bar);
             else
-                plane_load(is_v ? maps.v : maps.k, at, bar, 64 * half, row, kvh,
+                plane_load(is_v ? maps.v : maps.k, dst, bar, 64 * half, row, kvh,
                            page < 0 ? p.c.n_pages : page);
         }
         if constexpr (Q4) {
@@ -314,12 +336,14 @@ __device__ __forceinline__ void attn_feed(const AttnParams &p, const CacheMaps &
     }
 }
 
-// No copy is left in flight (only a wait that ran out could leave one).
+// No copy is left in flight (only a wait that ran out could leave one): the
+// stages filled last, behind `at`, become full.
 template <int STAGES, int DP, int NT>
-__device__ __forceinline__ void feed_end(RowsShared<DP, NT> &sh, int it)
+__device__ __forceinline__ void feed_end(RowsShared<DP, NT> &sh, RingAt<STAGES> at)
 {
-    for (int i = it > STAGES ? it - STAGES : 0; i < it; ++i)
-        for (uint32_t n = 0; n < kWaitLimit && !bar_try(&sh.full[i % STAGES], (i / STAGES) & 1); ++n) {
+    // of each stage the fill before `at`; a stage never filled counts as complete
+    for (int i = 0; i < STAGES; ++i, at.next())
+        for (uint32_t n = 0; n < kWaitLimit && !bar_try(&sh.full[at.st], at.phase ^ 1u); ++n) {
         }
 }
 
@@ -328,7 +352,7 @@ __device__ __forceinline__ void feed_end(RowsShared<DP, NT> &sh, int it)
 template <int DP, int NT, bool Q4>
 __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock &k, int kvh, int i0,
                                            int i1, RowsShared<DP, NT> &sh, const uint8_t *ring,
-                                           int *it)
+                                           RingAt<Rows<DP, Q4, NT>::kStages> *at)
 {
     using R = Rows<DP, Q4, NT>;
     constexpr int KS = DP / 16;       // k steps of S^T, m tiles of O^T
@@ -409,17 +433,28 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
     const int in1 = min(i1, k.c_sink + ((k.p_first + 1) >> sh_t) - k.c0);
     const int t0 = warp * U * 16;           // the warp's first key of a stage
     const int step = R::kKeys >> sh_t;      // tiles of a stage
+    constexpr int KEYS = R::kKeys;
+    const int gk = key_of<DP, Q4>(g);       // the lane's keys: gk, gk + 8 of K and S ...
+    const int vk[2] = {key_of<DP, Q4>(2 * c), key_of<DP, Q4>(2 * c + 1)};   // ... these, + 8 of V
+    // where the lane's operands lie in its warp's part of a stage
+    const int k_off = t0 * R::kRowPart + chunk_at<DP, Q4, KEYS>(gk, Q4 ? c * (DP / 8) >> 4 : c) +
+                      (Q4 ? c * (DP / 8) & 15 : 0);
+    const int k_off4 = t0 * R::kRowPart + chunk_at<DP, Q4, KEYS>(gk, 4 + c);   // bf16: dims 32 on
+    int v_off[2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+        v_off[y] = R::kPart + t0 * R::kRowPart +
+                   chunk_at<DP, Q4, KEYS>(vk[y], Q4 ? g * (DP / 16) >> 4 : g) +
+                   (Q4 ? g * (DP / 16) & 15 : 0);
+    const int s_off = 2 * R::kPart + (t0 + gk) * R::kScale;
     auto key_at = [&](int i, int t) {       // the token that is key t of the stage at tile i
         i += t >> sh_t;
         return i < i1 ? (k.tile_at(i) << sh_t) + (t & (p.tile - 1)) : INT_MAX / 2;
     };
-    constexpr int KEYS = R::kKeys;
-    const int gk = key_of<DP, Q4>(g);       // the lane's keys: gk, gk + 8 of K and S ...
-    const int vk[2] = {key_of<DP, Q4>(2 * c), key_of<DP, Q4>(2 * c + 1)};   // ... these, + 8 of V
 
-    for (int i = i0; i < i1; i += step, ++*it) {
-        const int st = *it % R::kStages;
-        bar_wait(&sh.full[st], (*it / R::kStages) & 1, &sh.abort);
+    for (int i = i0; i < i1; i += step, at->next()) {
+        const int st = at->st;
+        bar_wait(&sh.full[st], at->phase, &sh.abort);
         if (i + (t0 >> sh_t) < i1) {
         const uint8_t *stage = ring + st * R::kStageBytes;
         const bool full = i + (t0 >> sh_t) >= in0 && i + ((t0 + 16 * U - 1) >> sh_t) < in1;
@@ -428,7 +463,6 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
         float s[U][NT][4];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int tk = t0 + 16 * u + gk;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 s[u][n][0] = s[u][n][1] = s[u][n][2] = s[u][n][3] = 0.f;
@@ -436,9 +470,8 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
                 uint32_t kw[2][GR], ks[2][GR / 2];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const int b = c * (DP / 8);
-                    lds_words<GR>(kw[y], stage + chunk_at<DP, Q4, KEYS>(tk + 8 * y, b >> 4) + (b & 15));
-                    lds_words<GR / 2>(ks[y], stage + 2 * R::kPart + (tk + 8 * y) * R::kScale);
+                    lds_words<GR>(kw[y], stage + k_off + (16 * u + 8 * y) * R::kRowPart);
+                    lds_words<GR / 2>(ks[y], stage + s_off + (16 * u + 8 * y) * R::kScale);
                 }
 #pragma unroll
                 for (int w = 0; w < GR; ++w) {
@@ -466,8 +499,10 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
             } else {
 #pragma unroll
                 for (int w = 0; w < GR; ++w) {
-                    const uint4 a = *reinterpret_cast<const uint4 *>(stage + chunk_at<DP, Q4, KEYS>(tk, 4 * w + c));
-                    const uint4 b = *reinterpret_cast<const uint4 *>(stage + chunk_at<DP, Q4, KEYS>(tk + 8, 4 * w + c));
+                    const uint8_t *kp = stage + (w & 1 ? k_off4 : k_off) + (w >> 1) * (KEYS * 128) +
+                                        16 * u * R::kRowPart;
+                    const uint4 a = *reinterpret_cast<const uint4 *>(kp);
+                    const uint4 b = *reinterpret_cast<const uint4 *>(kp + 8 * R::kRowPart);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         mma16816(s[u][n], a.x, b.x, a.y, b.y, qf[n][2 * w][0], qf[n][2 * w][1]);
@@ -550,20 +585,16 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
             // the second of two tiles may lie beyond the piece: nothing was copied there
             if (u && i + ((t0 + 16 * u) >> sh_t) >= i1)
                 break;
-            const uint8_t *vpart = stage + R::kPart;
-            const int tk = t0 + 16 * u, j0 = full ? 0 : key_at(i, tk);
+            const int j0 = full ? 0 : key_at(i, t0 + 16 * u);
             if constexpr (Q4) {
                 uint32_t vw[4][GR / 2], vs[2][GR / 2];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int b = g * (DP / 16);
-                    lds_words<GR / 2>(
-                        vw[y], vpart + chunk_at<DP, Q4, KEYS>(tk + vk[y & 1] + 8 * (y >> 1), b >> 4) +
-                                   (b & 15));
-                }
+                for (int y = 0; y < 4; ++y)
+                    lds_words<GR / 2>(vw[y], stage + v_off[y & 1] +
+                                                 (16 * u + 8 * (y >> 1)) * R::kRowPart);
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
-                    lds_words<GR / 2>(vs[y], stage + 2 * R::kPart + (KEYS + tk + gk + 8 * y) * R::kScale);
+                    lds_words<GR / 2>(vs[y], stage + s_off + (KEYS + 16 * u + 8 * y) * R::kScale);
                 if (!full) {
                     // 0 * NaN: a key no row sees becomes zero; one that only some
                     // rows see must not reach the others
@@ -614,7 +645,8 @@ __device__ __forceinline__ void attn_piece(const AttnParams &p, const AttnBlock 
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
                         v[y] = *reinterpret_cast<const uint4 *>(
-                            vpart + chunk_at<DP, Q4, KEYS>(tk + vk[y & 1] + 8 * (y >> 1), 8 * h + g));
+                            stage + v_off[y & 1] + (16 * u + 8 * (y >> 1)) * R::kRowPart +
+                            h * (KEYS * 128));
                     if (!full) {
                         // 0 * NaN: a key no row sees becomes zero; one that only
                         // some rows see must not reach the others
@@ -754,10 +786,10 @@ attn_cluster_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         return;     // the whole cluster
     const int share = (k.ntiles + size - 1) / size;
     const int i0 = min(k.ntiles, rank * share), i1 = min(k.ntiles, i0 + share);
-    int it = 0;
+    RingAt<R::kStages> it;
     if (warp == kWarps) {
         attn_feed<DP, Q4, NT>(p, maps, k, kvh, i0, i1, sh, ring, &it);
-        feed_end<R::kStages>(sh, it);
+        feed_end(sh, it);
     } else
         attn_piece<DP, NT, Q4>(p, k, kvh, i0, i1, sh, ring, &it);
     for (int r = warp; warp < kWarps && r < k.nrows; r += kWarps) {
@@ -903,7 +935,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
     // The feeding warp and the computing ones walk the same pieces, each at its
     // own pace.
     const bool feeds = warp == kWarps;
-    int it = 0;
+    RingAt<R::kStages> it;
     bool first = true;
     while (at < end) {
         // the next sequence with rows of this launch
@@ -970,7 +1002,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
             ++b;
         }
     }    if (feeds)
-        feed_end<R::kStages>(sh, it);
+        feed_end(sh, it);
     else if (threadIdx.x == 0 && sh.abort)
         atomicOr(p.status, kStatusWait);
 }
