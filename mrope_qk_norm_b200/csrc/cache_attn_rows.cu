@@ -232,11 +232,12 @@ __device__ __forceinline__ void lds_words(uint32_t *w, const uint8_t *p)
     }
 }
 
-// Untiled copy of a run of scale rows.
+// Untiled copy of a run of scale rows; by a whole warp, as plane_load.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
     asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n}"
         ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
@@ -257,11 +258,7 @@ __device__ __forceinline__ void attn_feed(const AttnParams &p, const CacheMaps &
     const bool mine = first < R::kKeys;
     const bool is_v = Q4 ? kind & 1 : kind >= R::kHalves;
     const bool scales = Q4 && kind >= 2;
-    const int half = Q4 ? 0 : kind % R::kHalves;
-    const CachePlane &sp = is_v ? p.c.vs : p.c.ks;
-    const uint32_t part = is_v ? R::kPart : 0;
-    const uint32_t to = scales ? 2 * R::kPart + (is_v ? R::kKeys * R::kScale : 0) + first * R::kScale
-                               : part + half * (R::kKeys * 128) + first * R::kRowPart;
+    const uint32_t to = 2 * R::kPart + ((is_v ? R::kKeys : 0) + first) * R::kScale;   // scales
     const uint32_t bytes = scales ? box * R::kScale : box * R::kRowPart;
     const int32_t *table = p.table + (int64_t)k.b * p.table_stride;
     // this lane's run of keys in the stage at tile i: its page (-1: none; -2: no
@@ -282,7 +279,6 @@ __device__ __forceinline__ void attn_feed(const AttnParams &p, const CacheMaps &
     look(i0, &page, &row);
     for (int i = i0; i < i1; i += step, at->next()) {
         const int st = at->st;
-        const uint32_t dst = sm_u32(ring) + st * R::kStageBytes + to;
         const uint32_t bar = sm_u32(&sh.full[st]);
         int page_next, row_next;
         look(i + step, &page_next, &row_next);
@@ -306,13 +302,38 @@ __device__ __forceinline__ void attn_feed(const AttnParams &p, const CacheMaps &
         if (lane == 0)
             bar_expect(&sh.full[st], total);
         __syncwarp();
-        if (issue) {
-            if (scales)
-                bulk_load(dst, sp.base + kvh * sp.hs + (uint64_t)page * (uint32_t)sp.ps +
-                                  (uint64_t)(uint32_t)row * (uint32_t)sp.rs, bytes, bar);
-            else
-                plane_load(is_v ? maps.v : maps.k, dst, bar, 64 * half, row, kvh,
-                           page < 0 ? p.c.n_pages : page);
+        // copy x of the stage: lane x's
+        const int used = (R::kKeys >> p.tile_shift) * KINDS;
+        const unsigned go = __ballot_sync(0xffffffffu, issue);
+        const uint32_t stage = sm_u32(ring) + st * R::kStageBytes;
+        int c1, c2, c3;
+        plane_coords(is_v ? maps.v : maps.k, row, kvh, page < 0 ? p.c.n_pages : page, &c1, &c2, &c3);
+        const CachePlane &sp = is_v ? p.c.vs : p.c.ks;
+        const uint64_t from = reinterpret_cast<uint64_t>(sp.base) + kvh * sp.hs +
+                              (uint64_t)(uint32_t)max(page, 0) * (uint32_t)sp.ps +
+                              (uint64_t)(uint32_t)row * (uint32_t)sp.rs;
+        for (int f = 0; f < used; f += KINDS) {
+#pragma unroll
+            for (int kd = 0; kd < KINDS; ++kd) {
+                const int x = f + kd;
+                const bool v = Q4 ? kd & 1 : kd >= R::kHalves;
+                const int hf = Q4 ? 0 : kd % R::kHalves;
+                if (Q4 && kd >= 2) {
+                    const uint64_t a = __shfl_sync(0xffffffffu, from, x);
+                    if (go >> x & 1u)
+                        bulk_load(stage + 2 * R::kPart +
+                                      ((v ? R::kKeys : 0) + f / KINDS * box) * R::kScale,
+                                  reinterpret_cast<const void *>(a), box * R::kScale, bar);
+                } else {
+                    const int a1 = __shfl_sync(0xffffffffu, c1, x), a2 = __shfl_sync(0xffffffffu, c2, x),
+                              a3 = __shfl_sync(0xffffffffu, c3, x);
+                    if (go >> x & 1u)
+                        plane_copy(v ? maps.v : maps.k,
+                                   stage + (v ? R::kPart : 0) + hf * (R::kKeys * 128) +
+                                       f / KINDS * box * R::kRowPart,
+                                   bar, 64 * hf, a1, a2, a3);
+                }
+            }
         }
         if constexpr (Q4) {
             if (!p.dense_scales) {

@@ -50,6 +50,10 @@ namespace {
 
 constexpr int kTile = 128;               // keys of a tile, rows of a tile
 constexpr float kSlack = 8.f;
+constexpr int kPolyEvery = 4;
+constexpr float kExpC0 = 0.9999992847442627f, kExpC1 = 0.6931217908859253f,
+                kExpC2 = 0.240247443318367f, kExpC3 = 0.05591785907745361f,
+                kExpC4 = 0.009570100344717503f;
 constexpr uint32_t kWaitLimit = 1u << 21;
 
 template <int DP>
@@ -97,8 +101,8 @@ __device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity)
         : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
     return ok != 0;
 }
-// False when the wait ran out or another role's has.
-__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, int *abort)
+// By a whole warp.  False when the wait ran out or another role's has.
+__device__ __forceinline__ bool bar_wait_long(uint64_t *b, uint32_t parity, int *abort)
 {
     for (uint32_t i = 0; i < kWaitLimit; ++i) {
         if (bar_try(b, parity))
@@ -108,6 +112,12 @@ __device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, int *abor
     }
     *reinterpret_cast<volatile int *>(abort) = 1;
     return false;
+}
+__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, int *abort)
+{
+    if (__all_sync(0xffffffffu, bar_try(b, parity)))
+        return true;
+    return __all_sync(0xffffffffu, bar_wait_long(b, parity, abort));
 }
 
 __device__ __forceinline__ void fence_async()
@@ -122,10 +132,16 @@ __device__ __forceinline__ void tc_fence_after()
 {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
+// The tensor-core instructions below are issued by one elected lane of a whole,
+// converged warp.  Under `if (lane == 0)` the compiler cannot know that one lane
+// is active and wraps each in a loop over lanes: eight of them took 470 (P V) and
+// 750 clocks (Q K) to issue, more than they take to run.
 __device__ __forceinline__ void tc_commit(uint64_t *b)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     smem_u32(b)) : "memory");
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(
+            smem_u32(b)) : "memory");
 }
 
 // Shared-memory operand descriptors, 128-byte swizzle (bits 61-63 = 2), the
@@ -145,15 +161,15 @@ __device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t addr)
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int acc)
 {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+        "{\n .reg .pred p, e;\n setp.ne.u32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int acc)
 {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+        "{\n .reg .pred p, e;\n setp.ne.u32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
         ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
 
@@ -181,6 +197,63 @@ __device__ __forceinline__ void tm_store32(uint32_t addr, const uint32_t *r)
 __device__ __forceinline__ void tm_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Pairs of fp32 numbers in one register pair.
+__device__ __forceinline__ uint64_t pack_u2(uint32_t lo, uint32_t hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack_f2(float lo, float hi)
+{
+    return pack_u2(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ float f2_lo(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float f2_hi(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_bf2(uint64_t x) { return pack2(f2_lo(x), f2_hi(x)); }
+__device__ __forceinline__ float max3_nan(float a, float b, float c)   // NaN if any is
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t exp2_mufu2(uint64_t x)
+{
+    return pack_f2(exp2_fast(f2_lo(x)), exp2_fast(f2_hi(x)));
+}
+
+// 2^x for x <= 2^7 on the FMA pipe: x = n + f with n the nearest integer (the
+// rounding of x + 1.5 * 2^23, whose low bits are n), 2^f by the polynomial of
+// degree 4 with the least relative error on [-1/2, 1/2] (Remez; 2.7e-6, a
+// thousandth of the bf16 rounding that follows), n added to the exponent.  x
+// below -126 counts as -126.
+__device__ __forceinline__ uint64_t exp2_poly2(uint64_t x)
+{
+    const uint64_t big = pack_f2(12582912.f, 12582912.f), nbig = pack_f2(-12582912.f, -12582912.f);
+    x = pack_f2(fmaxf(f2_lo(x), -126.f), fmaxf(f2_hi(x), -126.f));
+    const uint64_t t = add_f2(x, big);
+    const uint64_t f = fma_f2(add_f2(t, nbig), pack_f2(-1.f, -1.f), x);
+    uint64_t r = pack_f2(kExpC4, kExpC4);
+    r = fma_f2(r, f, pack_f2(kExpC3, kExpC3));
+    r = fma_f2(r, f, pack_f2(kExpC2, kExpC2));
+    r = fma_f2(r, f, pack_f2(kExpC1, kExpC1));
+    r = fma_f2(r, f, pack_f2(kExpC0, kExpC0));
+    return pack_u2((uint32_t)r + ((uint32_t)t << 23), (uint32_t)(r >> 32) + ((uint32_t)(t >> 32) << 23));
+}
+
 template <int REGS>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS)); }
 template <int REGS>
@@ -194,6 +267,28 @@ __device__ __forceinline__ uint4 pair_order(const uint4 &v)
     return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
                       __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
 }
+
+// Row r of a block, its token and query head; steps without dividing.
+struct RowWalk {
+    int r, G, h0, h;
+    int64_t t;
+    __device__ __forceinline__ RowWalk(const AttnParams &p, const AttnBlock &k, int kvh, int first)
+        : r(first), G(p.G), h0(kvh * p.G)
+    {
+        const int row = k.row0 + first;
+        t = k.t0 + row / G;
+        h = h0 + row % G;
+    }
+    __device__ __forceinline__ void step(int n)
+    {
+        r += n;
+        h += n;
+        while (h >= h0 + G) {
+            h -= G;
+            ++t;
+        }
+    }
+};
 
 template <int DP, bool Q4>
 __global__ void __launch_bounds__(Q4 ? 512 : 384, 1)
@@ -260,28 +355,33 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // lane offset of the warp: 32 << 16
         const bool live = r < k.nrows;
         const int pos = live ? k.L - k.n + (k.row0 + r) / p.G : -1;
-        // Q row into its K-major tile; a negative scale goes into Q's signs
+        // The warp's 32 rows of Q into the K-major tile, whole rows at a time (a
+        // thread to a row costs 32 cache lines an instruction: 9 us a block); a
+        // negative scale goes into Q's signs.
+        constexpr int CH = DP / 8, AT_ONCE = 32 / CH;   // 16-byte chunks of a row, rows at once
+        const int r_warp = r - lane, ch = lane % CH;
         {
-            int64_t t;
-            int qh;
-            attn_row_of(p, k, kvh, live ? r : 0, &t, &qh);
-            const __nv_bfloat16 *src = p.q + t * p.q_ts + qh * p.q_hs;
-            const int row = r & (kTile - 1);
-            uint8_t *dst = base + h * Lay::kStageBytes + row * 128;
             const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+            constexpr int N = 32 / AT_ONCE;
+            uint4 v[N];
+            RowWalk at(p, k, kvh, r_warp + lane / CH);
 #pragma unroll
-            for (int ch = 0; ch < DP / 8; ++ch) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (live && 8 * ch < p.c.D)
-                    v = ld_stream(src + 8 * ch);
-                v.x ^= flip;
-                v.y ^= flip;
-                v.z ^= flip;
-                v.w ^= flip;
+            for (int i = 0; i < N; ++i, at.step(AT_ONCE)) {
+                v[i] = make_uint4(0, 0, 0, 0);
+                if (at.r < k.nrows && 8 * ch < p.c.D)
+                    v[i] = ld_stream(p.q + at.t * p.q_ts + at.h * p.q_hs + 8 * ch);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int row = (r_warp + i * AT_ONCE + lane / CH) & (kTile - 1);
+                v[i].x ^= flip;
+                v[i].y ^= flip;
+                v[i].z ^= flip;
+                v[i].w ^= flip;
                 if constexpr (Q4)
-                    v = pair_order(v);
-                *reinterpret_cast<uint4 *>(dst + (ch >> 3) * (kTile * 128) +
-                                           (((ch & 7) ^ (row & 7)) << 4)) = v;
+                    v[i] = pair_order(v[i]);
+                *reinterpret_cast<uint4 *>(base + h * Lay::kStageBytes + (ch >> 3) * (kTile * 128) +
+                                           row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = v[i];
             }
             fence_async();
             bar_arrive(&sh.q_full);
@@ -294,63 +394,108 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             for (int j = 0; j < nt && ok; ++j) {
                 const int j0 = k.tile_at(i0 + j) * kTile;
                 ok = bar_wait(&sh.s_full[h], j & 1, &sh.abort);
-                ok = __all_sync(0xffffffffu, ok);
                 if (!ok)
                     break;
                 tc_fence_after();
-                uint32_t s[kTile];
+                uint32_t pk[kTile / 2];     // the weights, bf16 pairs
+                float sum = 0.f;
+                const bool full = attn_all_see(p, k, j0, kTile);
+                bool again = !full || j == 0;
+                if (!again) {
+                    // Against the reference as it stands, in one pass: where the
+                    // maximum then turns out to exceed it by too much (or a score
+                    // is NaN) the tile is done again below.
+                    float mx = -INFINITY;
+                    uint64_t sum2[2] = {0, 0};
+                    const uint64_t sc2 = pack_f2(scale, scale), rf2 = pack_f2(-m, -m);
+                    uint32_t s[2][32];
+                    tm_load32(s[0], tm_s[h] + lanes);
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tm_load32(s + 32 * c, tm_s[h] + lanes + 32 * c);
-                tm_wait_load();
-                if (!attn_all_see(p, k, j0, kTile)) {
-                    const int hi_c = pos - j0, lo_c = lo_r - j0, sink_c = p.n_sink - j0;
+                    for (int c = 0; c < 4; ++c) {
+                        tm_wait_load();
+                        if (c < 3)
+                            tm_load32(s[(c + 1) & 1], tm_s[h] + lanes + 32 * (c + 1));
+                        const uint32_t *v = s[c & 1];
 #pragma unroll
-                    for (int c = 0; c < kTile; ++c)
-                        if (!(c <= hi_c && (c >= lo_c || c < sink_c)))
-                            s[c] = 0xff800000u;
+                        for (int e = 0; e < 32; e += 2) {
+                            mx = max3_nan(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                            uint64_t x = fma_f2(pack_u2(v[e], v[e + 1]), sc2, rf2);
+                            // every kPolyEvery-th pair on the FMA pipe
+                            x = (e / 2) % kPolyEvery == kPolyEvery - 1 ? exp2_poly2(x) : exp2_mufu2(x);
+                            sum2[(e >> 1) & 1] = add_f2(sum2[(e >> 1) & 1], x);
+                            pk[16 * c + e / 2] = pack_bf2(x);
+                        }
+                    }
+                    const uint64_t both = add_f2(sum2[0], sum2[1]);
+                    sum = f2_lo(both) + f2_hi(both);
+                    again = __any_sync(0xffffffffu, !(mx * scale <= m + kSlack));
                 }
-                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if (again) {
+                    const int hi_c = pos - j0, lo_c = lo_r - j0, sink_c = p.n_sink - j0;
+                    auto load = [&](uint32_t *v, int c) {
+                        tm_load32(v, tm_s[h] + lanes + 32 * c);
+                        tm_wait_load();
+                        if (!full) {
 #pragma unroll
-                for (int c = 0; c < kTile; ++c)
-                    mx4[c & 3] = fmaxf(mx4[c & 3], __uint_as_float(s[c]));
-                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * scale;
-                if (__any_sync(0xffffffffu, mx > m + kSlack)) {
-                    const float mn = fmaxf(m, mx);
-                    const float f = m == -INFINITY ? 0.f : exp2_fast(m - mn);
-                    m = mn;
-                    l *= f;
-                    if (j) {
+                            for (int e = 0; e < 32; ++e) {
+                                const int t = 32 * c + e;
+                                if (!(t <= hi_c && (t >= lo_c || t < sink_c)))
+                                    v[e] = 0xff800000u;
+                            }
+                        }
+                    };
+                    float mx = -INFINITY;
 #pragma unroll
-                        for (int c = 0; c < DP / 32; ++c) {
-                            uint32_t o[32];
-                            tm_load32(o, tm_o[h] + lanes + 32 * c);
-                            tm_wait_load();
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        load(v, c);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tm_store32(tm_o[h] + lanes + 32 * c, o);
+                        for (int e = 0; e < 32; ++e)
+                            mx = fmaxf(mx, __uint_as_float(v[e]));
+                    }
+                    mx *= scale;
+                    if (__any_sync(0xffffffffu, mx > m + kSlack)) {
+                        const float mn = fmaxf(m, mx);
+                        const float f = m == -INFINITY ? 0.f : exp2_fast(m - mn);
+                        m = mn;
+                        l *= f;
+                        if (j) {
+#pragma unroll
+                            for (int c = 0; c < DP / 32; ++c) {
+                                uint32_t o[32];
+                                tm_load32(o, tm_o[h] + lanes + 32 * c);
+                                tm_wait_load();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tm_store32(tm_o[h] + lanes + 32 * c, o);
+                            }
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    sum = 0.f;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        load(v, c);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float a = exp2_fast(fmaf(__uint_as_float(v[e]), scale, -ref));
+                            const float b = exp2_fast(fmaf(__uint_as_float(v[e + 1]), scale, -ref));
+                            sum += a + b;
+                            pk[16 * c + e / 2] = pack2(a, b);
                         }
                     }
                 }
-                const float ref = m == -INFINITY ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int c = 0; c < kTile; c += 2) {
-                    const float a = exp2_fast(fmaf(__uint_as_float(s[c]), scale, -ref));
-                    const float b = exp2_fast(fmaf(__uint_as_float(s[c + 1]), scale, -ref));
-                    sum[(c >> 1) & 3] += a + b;
-                    s[c >> 1] = pack2(a, b);
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tm_store32(tm_s[h] + lanes, s);
-                tm_store32(tm_s[h] + lanes + 32, s + 32);
+                l += sum;
+                tm_store32(tm_s[h] + lanes, pk);
+                tm_store32(tm_s[h] + lanes + 32, pk + 32);
                 tm_wait_store();
                 tc_fence_before();
                 bar_arrive(&sh.p_full[h]);
             }
             if (nt > 0 && ok)
-                ok = __all_sync(0xffffffffu, bar_wait(&sh.o_full[h], 0, &sh.abort));
+                ok = bar_wait(&sh.o_full[h], 0, &sh.abort);
             tc_fence_after();
             const bool only = nparts == 1;
             const bool poison = *reinterpret_cast<volatile int *>(&sh.poison) != 0;
@@ -361,51 +506,99 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                     attn_emit<E>(p, k, kvh, rr, part, only, pm, pl, po);
                 }
             } else {
-                int64_t t;
-                int qh;
-                attn_row_of(p, k, kvh, live ? r : 0, &t, &qh);
+                // O through shared memory (Q's tile is free), so that whole rows are
+                // written at a time: 64 dims in fp32 or all in bf16, the warp's rows
                 const bool empty = pos < 0;
-                const float inv = 1.f / l;
-                const int64_t wrow = ((int64_t)part * p.T + t) * p.Hq + qh;
+                const float inv = empty ? 0.f : 1.f / l;
+                uint8_t *slab = base + h * Lay::kStageBytes + (r_warp & (kTile - 1)) * (Lay::kHalves * 128);
+                if (only) {
+                    constexpr int ROW = Lay::kHalves * 128;
 #pragma unroll
-                for (int c = 0; c < DP / 32; ++c) {
-                    uint32_t o[32];
-                    __syncwarp();
-                    if (nt > 0) {
-                        tm_load32(o, tm_o[h] + lanes + 32 * c);
-                        tm_wait_load();
-                    } else {
+                    for (int c = 0; c < DP / 32; ++c) {
+                        uint32_t o[32];
+                        if (nt > 0) {
+                            tm_load32(o, tm_o[h] + lanes + 32 * c);
+                            tm_wait_load();
+                        }
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            o[e] = 0u;
+                        for (int g = 0; g < 4; ++g) {
+                            float f[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const int at = Q4 ? (e < 4 ? 2 * e : 2 * e - 7) : e;
+                                f[e] = nt == 0 || empty ? 0.f : __uint_as_float(o[8 * g + at]) * inv;
+                            }
+                            const int x = 4 * c + g;
+                            *reinterpret_cast<uint4 *>(slab + lane * ROW + (x >> 3) * 128 +
+                                                       (((x & 7) ^ (lane & 7)) << 4)) = pack8(f);
+                        }
                     }
+                    __syncwarp();
+                    RowWalk at(p, k, kvh, r_warp + lane / CH);
+                    constexpr int N = 8;        // rows a lane has in flight
+                    for (int i0 = 0; i0 < 32; i0 += N * AT_ONCE) {
+                        uint4 v[N];
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const int d = 32 * c + 8 * g;
-                        if (!live || d >= p.c.D)
-                            continue;
-                        float f[8];
+                        for (int i = 0; i < N; ++i) {
+                            const int rl = i0 + i * AT_ONCE + lane / CH;
+                            v[i] = *reinterpret_cast<const uint4 *>(
+                                slab + rl * ROW + (ch >> 3) * 128 + (((ch & 7) ^ (rl & 7)) << 4));
+                        }
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int at = Q4 ? (e < 4 ? 2 * e : 2 * e - 7) : e;
-                            f[e] = __uint_as_float(o[8 * g + at]);
-                            if (only)
-                                f[e] = empty ? 0.f : f[e] * inv;
+                        for (int i = 0; i < N; ++i, at.step(AT_ONCE))
+                            if (at.r < k.nrows && 8 * ch < p.c.D)
+                                *reinterpret_cast<uint4 *>(p.out + at.t * p.o_ts +
+                                                           (int64_t)at.h * p.c.D + 8 * ch) = v[i];
+                    }
+                } else {
+                    // 32 dims of fp32 at a time: 128-byte rows, 8 lanes each
+#pragma unroll
+                    for (int c = 0; c < DP / 32; ++c) {
+                        uint32_t o[32];
+                        if (nt > 0) {
+                            tm_load32(o, tm_o[h] + lanes + 32 * c);
+                            tm_wait_load();
                         }
-                        if (only) {
-                            *reinterpret_cast<uint4 *>(p.out + t * p.o_ts + (int64_t)qh * p.c.D +
-                                                       d) = pack8(f);
-                        } else {
-                            float4 *w = reinterpret_cast<float4 *>(p.ws_o + wrow * p.c.D + d);
-                            w[0] = make_float4(f[0], f[1], f[2], f[3]);
-                            w[1] = make_float4(f[4], f[5], f[6], f[7]);
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            uint32_t f[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const int at = Q4 ? (e < 4 ? 2 * e : 2 * e - 7) : e;
+                                f[e] = nt == 0 ? 0u : o[8 * g + at];
+                            }
+                            uint8_t *d = slab + lane * 128;
+                            *reinterpret_cast<uint4 *>(d + (((2 * g) ^ (lane & 7)) << 4)) =
+                                make_uint4(f[0], f[1], f[2], f[3]);
+                            *reinterpret_cast<uint4 *>(d + (((2 * g + 1) ^ (lane & 7)) << 4)) =
+                                make_uint4(f[4], f[5], f[6], f[7]);
                         }
+                        __syncwarp();
+                        RowWalk at(p, k, kvh, r_warp + lane / 8);
+                        uint4 v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int rl = 4 * i + lane / 8;
+                            v[i] = *reinterpret_cast<const uint4 *>(
+                                slab + rl * 128 + (((lane & 7) ^ (rl & 7)) << 4));
+                        }
+                        const int d = 32 * c + 4 * (lane & 7);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i, at.step(4))
+                            if (at.r < k.nrows && d < p.c.D) {
+                                const int64_t row = ((int64_t)part * p.T + at.t) * p.Hq + at.h;
+                                *reinterpret_cast<uint4 *>(p.ws_o + row * p.c.D + d) = v[i];
+                            }
+                        __syncwarp();
                     }
                 }
-                if (live) {
+                if (live && (!only || p.lse)) {
+                    int64_t t;
+                    int qh;
+                    attn_row_of(p, k, kvh, r, &t, &qh);
                     if (!only)
-                        p.ws_ml[wrow] = make_float2(m, l);
-                    else if (p.lse)
+                        p.ws_ml[((int64_t)part * p.T + t) * p.Hq + qh] = make_float2(m, l);
+                    else
                         p.lse[t * p.Hq + qh] =
                             empty ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
                 }
@@ -414,82 +607,87 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     } else {
     regs_down<72>();
     if (warp == 8) {
-        // ================================================ matrix instructions, one lane
-        if (lane == 0) {
-            constexpr uint32_t kId = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(kTile / 16) << 24;
-            constexpr uint32_t kIdS = kId | (uint32_t)(kTile / 8) << 17;
-            constexpr uint32_t kIdO = kId | 1u << 16 | (uint32_t)(DP / 8) << 17;
-            const uint64_t dk = desc_base(16), dv = desc_base(kTile * 128);
-            const uint32_t q_at = smem_u32(base), ring_at = smem_u32(ring);
-            bool ok = bar_wait(&sh.q_full, 0, &sh.abort);
-            for (int j = -1; j < nt && ok; ++j) {
-                // items of the ring: K(0) V(0) K(1) V(1) ...
-                const int iv = 2 * j + 1, ik = 2 * j + 2;
-                const int sv = iv % NST, sk = ik % NST;
+        // ================================================ matrix instructions
+        constexpr uint32_t kId = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(kTile / 16) << 24;
+        constexpr uint32_t kIdS = kId | (uint32_t)(kTile / 8) << 17;
+        constexpr uint32_t kIdO = kId | 1u << 16 | (uint32_t)(DP / 8) << 17;
+        // descriptors in units of 16 bytes; the address field never carries over
+        const uint64_t dq = desc_at(desc_base(16), smem_u32(base));
+        const uint64_t dk = desc_at(desc_base(16), smem_u32(ring));
+        const uint64_t dv = desc_at(desc_base(kTile * 128), smem_u32(ring));
+        constexpr uint32_t kStage16 = Lay::kStageBytes / 16;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        int sk = 0, sv = 0;                 // stages of K(j + 1) and V(j): K(0) V(0) K(1) V(1) ...
+        uint32_t pk = 0, pv = 0;
+        auto step = [&](int *st, uint32_t *ph, int by) {
+            *st += by;
+            if (*st >= NST) {
+                *st -= NST;
+                *ph ^= 1u;
+            }
+        };
+        step(&sv, &pv, 1);
+        bool ok = bar_wait(&sh.q_full, 0, &sh.abort);
+        for (int j = -1; j < nt && ok; ++j) {
+            const bool next = j + 1 < nt;
+            if (j >= 0)
+                ok = bar_wait(&sh.raw[sv], pv, &sh.abort);
+            for (int h = 0; h < halves && ok; ++h) {
+                const uint32_t s_at = tm + 128 * h, o_at = tm + 256 + DP * h;
                 if (j >= 0) {
-                    ok = bar_wait(&sh.raw[sv], (iv / NST) & 1, &sh.abort);
+                    ok = bar_wait(&sh.p_full[h], j & 1, &sh.abort);
                     if (!ok)
                         break;
-                }
-                const bool next = j + 1 < nt;
-                bool have_k = false;
-                for (int h = 0; h < halves && ok; ++h) {
-                    if (j >= 0) {
-                        ok = bar_wait(&sh.p_full[h], j & 1, &sh.abort);
-                        if (!ok)
-                            break;
-                        tc_fence_after();
+                    tc_fence_after();
+                    const uint64_t b = dv + sv * kStage16;
 #pragma unroll
-                        for (int s = 0; s < kTile / 16; ++s)
-                            mma_ts(tm_o[h], tm_s[h] + 8 * s,
-                                   desc_at(dv, ring_at + sv * Lay::kStageBytes + s * 2048), kIdO,
-                                   j > 0 || s > 0);
-                        if (!next)
-                            tc_commit(&sh.o_full[h]);
-                    }
-                    if (next) {
-                        if (!have_k) {
-                            ok = bar_wait(&sh.raw[sk], (ik / NST) & 1, &sh.abort);
-                            if (!ok)
-                                break;
-                            tc_fence_after();
-                            have_k = true;
-                        }
-#pragma unroll
-                        for (int s = 0; s < DP / 16; ++s) {
-                            const uint32_t off = (s >> 2) * (kTile * 128) + (s & 3) * 32;
-                            mma_ss(tm_s[h], desc_at(dk, q_at + h * Lay::kStageBytes + off),
-                                   desc_at(dk, ring_at + sk * Lay::kStageBytes + off), kIdS, s > 0);
-                        }
-                        tc_commit(&sh.s_full[h]);
-                    }
+                    for (int s = 0; s < kTile / 16; ++s)
+                        mma_ts(o_at, s_at + 8 * s, b + s * 128, kIdO, j > 0 || s > 0);
+                    if (!next)
+                        tc_commit(&sh.o_full[h]);
                 }
-                if (!ok)
-                    break;
-                if (j >= 0)
-                    tc_commit(&sh.empty[sv]);
-                if (next)
-                    tc_commit(&sh.empty[sk]);
+                if (next) {
+                    if (h == 0)
+                        ok = bar_wait(&sh.raw[sk], pk, &sh.abort);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint64_t a = dq + h * kStage16, b = dk + sk * kStage16;
+#pragma unroll
+                    for (int s = 0; s < DP / 16; ++s) {
+                        const uint32_t off = (s >> 2) * (kTile * 8) + (s & 3) * 2;
+                        mma_ss(s_at, a + off, b + off, kIdS, s > 0);
+                    }
+                    tc_commit(&sh.s_full[h]);
+                }
             }
-            tc_commit(&sh.drain);
-            // everything issued has finished, whatever became of the rest
-            for (uint32_t i = 0; i < kWaitLimit && !bar_try(&sh.drain, 0); ++i) {
+            if (!ok)
+                break;
+            if (j >= 0) {
+                tc_commit(&sh.empty[sv]);
+                step(&sv, &pv, 2);
+            }
+            if (next) {
+                tc_commit(&sh.empty[sk]);
+                step(&sk, &pk, 2);
             }
         }
-        __syncwarp();
+        tc_commit(&sh.drain);
+        // everything issued has finished, whatever became of the rest
+        for (uint32_t i = 0; i < kWaitLimit && !__all_sync(0xffffffffu, bar_try(&sh.drain, 0)); ++i) {
+        }
     } else if (!Q4 && warp == 9) {
         // ================================================ TMA
-        // A lane owns one copy of a tile: `box` keys, 64 dims.  It looks its page
-        // up once for K and V and asks for the next tile's before it waits.
-        const int copies = kTile / map.k.box * Lay::kHalves;
-        const int hf = lane % Lay::kHalves, c = lane / Lay::kHalves * map.k.box;
+        // A lane looks up one run of `box` keys of a tile, once for K and V, and
+        // asks for the next tile's before it waits.
+        const int box = map.k.box, copies = kTile / box, c = lane * box;
         const bool mine = lane < copies;
         auto look = [&](int j, int *page, int *row) {
             // a copy no row sees any key of reads zeros: a page past the last
-            const int a = k.tile_at(i0 + j) * kTile + c, z = a + map.k.box;
+            const int a = k.tile_at(i0 + j) * kTile + c, z = a + box;
             *page = -1;
             if (mine && j < nt && ((a < k.hi && z > k.lo) || a < k.sink))
-                *page = attn_page(p, k.b, a, hf == 0);
+                *page = attn_page(p, k.b, a, true);
             if (*page < 0)
                 *page = p.c.n_pages;
             *row = a % p.c.page_size;
@@ -505,7 +703,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                 look((it >> 1) + 1, &page_next, &row_next);
             if (it >= NST)
                 ok = bar_wait(&sh.empty[st], (it / NST - 1) & 1, &sh.abort);
-            if (!__all_sync(0xffffffffu, ok))
+            if (!ok)
                 break;
             // the values of a tile that not every row sees go past a clearing warp
             uint64_t *bar = &sh.raw[st];
@@ -514,10 +712,18 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             if (lane == 0)
                 bar_expect(bar, Lay::kStageBytes);
             __syncwarp();
-            if (mine) {
-                plane_load(is_v ? map.v : map.k,
-                           smem_u32(ring + st * Lay::kStageBytes + hf * kTile * 128) + c * 128,
-                           smem_u32(bar), 64 * hf, row, kvh, page);
+            const uint32_t stage = smem_u32(ring) + st * Lay::kStageBytes;
+            const PlaneMap &map_of = is_v ? map.v : map.k;
+            int c1, c2, c3;
+            plane_coords(map_of, row, kvh, page, &c1, &c2, &c3);
+#pragma unroll 2
+            for (int x = 0; x < copies; ++x) {
+                const int a1 = __shfl_sync(0xffffffffu, c1, x), a2 = __shfl_sync(0xffffffffu, c2, x),
+                          a3 = __shfl_sync(0xffffffffu, c3, x);
+#pragma unroll
+                for (int hf = 0; hf < Lay::kHalves; ++hf)
+                    plane_copy(map_of, stage + hf * (kTile * 128) + x * (box * 128), smem_u32(bar),
+                               64 * hf, a1, a2, a3);
             }
             if (is_v) {
                 page = page_next;
@@ -547,27 +753,40 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             if ((e & 1) != warp - 10)
                 continue;
             const int st = (2 * j + 1) % NST;
-            if (!__all_sync(0xffffffffu, bar_wait(&sh.land[e & 3], (e >> 2) & 1, &sh.abort)))
+            if (!bar_wait(&sh.land[e & 3], (e >> 2) & 1, &sh.abort))
                 break;
             uint8_t *tile = ring + st * Lay::kStageBytes;
-            bool bad = false;
-            // 4 rows of 128 bytes at a time, 8 lanes each
+            // keys no row sees: [z0, z1) and [z2, 128)
+            const int z0 = min(kTile, max(0, k.sink - j0)), z1 = min(kTile, max(z0, k.lo - j0));
+            const int z2 = min(kTile, max(z1, k.hi - j0));
+            auto clear = [&](int from, int to) {
+                for (int x = from * Lay::kHalves * 8 + lane; x < to * Lay::kHalves * 8; x += 32)
+                    *reinterpret_cast<uint4 *>(tile + (x >> 3) % Lay::kHalves * (kTile * 128) +
+                                               (x >> 3) / Lay::kHalves * 128 + (x & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+            };
+            clear(z0, z1);
+            clear(z2, kTile);
+            // keys that only some rows see: after the first position, or before the
+            // last one's window (the largest magnitude of each half word shows them)
+            uint32_t top = 0;
+            auto scan = [&](int from, int to) {
 #pragma unroll 4
-            for (int rr = lane >> 3; rr < kTile; rr += 4) {
-                const bool seen = attn_block_sees(k, j0 + rr);
-#pragma unroll
-                for (int hf = 0; hf < Lay::kHalves; ++hf) {
-                    uint4 *at = reinterpret_cast<uint4 *>(tile + hf * kTile * 128 + rr * 128 +
-                                                          (lane & 7) * 16);
-                    if (!seen) {
-                        *at = make_uint4(0, 0, 0, 0);
-                    } else if (mixed) {
-                        const uint4 v = *at;
-                        bad |= nonfinite2(v.x) | nonfinite2(v.y) | nonfinite2(v.z) | nonfinite2(v.w);
-                    }
+                for (int x = from * Lay::kHalves * 8 + lane; x < to * Lay::kHalves * 8; x += 32) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(
+                        tile + (x >> 3) % Lay::kHalves * (kTile * 128) +
+                        (x >> 3) / Lay::kHalves * 128 + (x & 7) * 16);
+                    top = __vmaxu2(__vmaxu2(top, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
+                                   __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
                 }
+            };
+            if (mixed) {
+                const int after = min(kTile, max(0, k.p_first + 1 - j0));
+                const int within = p.window ? min(kTile, max(0, k.p_last - p.window + 1 - j0)) : 0;
+                scan(0, min(within, after));
+                scan(max(after, 0), z2);
             }
-            if (bad)
+            if ((top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u)
                 *reinterpret_cast<volatile int *>(&sh.poison) = 1;
             fence_async();
             __syncwarp();
@@ -620,7 +839,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             const int st = it % NST;
             const bool is_v = it & 1;
             if (it >= NST) {
-                ok = __all_sync(0xffffffffu, bar_wait(&sh.empty[st], (it / NST - 1) & 1, &sh.abort));
+                ok = bar_wait(&sh.empty[st], (it / NST - 1) & 1, &sh.abort);
                 if (!ok)
                     break;
             }
