@@ -8,17 +8,20 @@
 // P_i (bf16) takes the place of S_i there, so neither passes through shared
 // memory.  Tensor memory: S0 | S1 | O0 | O1.
 //
-// The softmax warps take registers from the others (setmaxnreg): 216 + 216 + 72
-// of the 3 x 168 launched (4 bits: 184 + 184 + 72 + 72 of 4 x 128), so a row's 128
-// scores stay in registers.
+// Two threads share a row, 64 scores each, because the softmax's latency is what
+// the tensor cores wait for (one thread a row: 3470 clocks per 128 keys of a
+// block, 2048 of which the tensor cores work); the two agree on the reference
+// through a named barrier.  The softmax warps take registers from the others
+// (setmaxnreg): 4 x 104 + 64 of the 5 x 96 launched (4 bits: 4 x 88 + 2 x 64 of
+// 6 x 80).
 //
-//   warps 0-3, 4-7  softmax of tile 0 and tile 1, one row a thread
-//   warp 8          issues the matrix instructions, in the order
+//   warps 0-15      softmax: 0-7 of tile 0, 8-15 of tile 1
+//   warp 16         issues the matrix instructions, in the order
 //                   P0 V(j), Q0 K(j+1), P1 V(j), Q1 K(j+1): while one tile's
 //                   softmax runs, the tensor cores work for the other
-//   bf16: warp 9    K and V tiles by TMA, a ring of 32 KB (16 KB) stages
-//         10, 11    clear the values no row of the block sees (below)
-//   4 bits: 12-15   K and V tiles from nibbles to bf16 in shared memory, one
+//   bf16: warp 17   K and V tiles by TMA, a ring of 32 KB (16 KB) stages
+//         18, 19    clear the values no row of the block sees (below)
+//   4 bits: 20-23   K and V tiles from nibbles to bf16 in shared memory, one
 //                   key a thread
 //
 // Per tile and 128 keys at D = 128 the two products take 1024 clocks of the
@@ -48,6 +51,8 @@
 namespace qkr {
 namespace {
 
+constexpr int kSoftWarps = 16;
+constexpr int tiles_threads(bool q4) { return 32 * (kSoftWarps + (q4 ? 8 : 4)); }
 constexpr int kTile = 128;               // keys of a tile, rows of a tile
 constexpr float kSlack = 8.f;
 constexpr int kPolyEvery = 4;
@@ -56,21 +61,24 @@ constexpr float kExpC0 = 0.9999992847442627f, kExpC1 = 0.6931217908859253f,
                 kExpC4 = 0.009570100344717503f;
 constexpr uint32_t kWaitLimit = 1u << 21;
 
-template <int DP>
-struct Layout {
-    static constexpr int kHalves = DP / 64;
-    static constexpr int kStageBytes = kHalves * kTile * 128;
-    static constexpr int kQBytes = 2 * kStageBytes;
-    static constexpr int kStages = DP == 128 ? 5 : 8;
-    static constexpr int kBytes = kQBytes + kStages * kStageBytes + 1024 /* alignment */;
-};
-
 struct Shared {
     uint64_t raw[8], empty[8];            // ring: full, free
     uint64_t land[4];                     // a V tile to be cleared first has landed, in turn
     uint64_t q_full, s_full[2], p_full[2], o_full[2], drain;
     uint32_t tmem;
     int abort, poison;
+    int sick[kSoftWarps];
+    int over[2][kSoftWarps];              // a half's maximum is out of reach, by parity of the tile
+    float half[2][2][kTile];              // a half row's maximum or sum: tile, half, row
+};
+
+template <int DP>
+struct Layout {
+    static constexpr int kHalves = DP / 64;
+    static constexpr int kStageBytes = kHalves * kTile * 128;
+    static constexpr int kQBytes = 2 * kStageBytes;
+    static constexpr int kStages = DP == 128 ? 5 : 8;
+    static constexpr int kBytes = kQBytes + kStages * kStageBytes + (int)sizeof(Shared);
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p)
@@ -181,12 +189,18 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
     "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, " \
     "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}"
 
-// 32 columns of the warp's 32 lanes, one lane a thread.
-__device__ __forceinline__ void tm_load32(uint32_t *r, uint32_t addr)
+// 16 or 32 columns of the warp's 32 lanes, one lane a thread.
+#define QKR_LIST16                                                                               \
+    "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}"
+__device__ __forceinline__ void tm_load16(uint32_t *r, uint32_t addr)
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 " QKR_LIST32 ", [%32];"
-                 : QKR_R8(r, 0), QKR_R8(r, 8), QKR_R8(r, 16), QKR_R8(r, 24)
-                 : "r"(addr));
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 " QKR_LIST16 ", [%16];"
+                 : QKR_R8(r, 0), QKR_R8(r, 8) : "r"(addr));
+}
+__device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], " QKR_LIST16 ";" ::QKR_I8(r, 0),
+                 QKR_I8(r, 8), "r"(addr) : "memory");
 }
 __device__ __forceinline__ void tm_store32(uint32_t addr, const uint32_t *r)
 {
@@ -268,39 +282,16 @@ __device__ __forceinline__ uint4 pair_order(const uint4 &v)
                       __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
 }
 
-// Row r of a block, its token and query head; steps without dividing.
-struct RowWalk {
-    int r, G, h0, h;
-    int64_t t;
-    __device__ __forceinline__ RowWalk(const AttnParams &p, const AttnBlock &k, int kvh, int first)
-        : r(first), G(p.G), h0(kvh * p.G)
-    {
-        const int row = k.row0 + first;
-        t = k.t0 + row / G;
-        h = h0 + row % G;
-    }
-    __device__ __forceinline__ void step(int n)
-    {
-        r += n;
-        h += n;
-        while (h >= h0 + G) {
-            h -= G;
-            ++t;
-        }
-    }
-};
-
 template <int DP, bool Q4>
-__global__ void __launch_bounds__(Q4 ? 512 : 384, 1)
+__global__ void __launch_bounds__(tiles_threads(Q4), 1)
 attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CacheMaps map)
 {
     using Lay = Layout<DP>;
     constexpr int NST = Lay::kStages;
     constexpr int E = DP / 32;
-    extern __shared__ uint8_t dyn[];
-    __shared__ Shared sh;
-    uint8_t *base = reinterpret_cast<uint8_t *>(((uintptr_t)dyn + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t base[];   // Q, ring, the rest
     uint8_t *ring = base + Lay::kQBytes;
+    Shared &sh = *reinterpret_cast<Shared *>(ring + NST * Lay::kStageBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     pdl_wait();
@@ -318,6 +309,11 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     const int nt = min(k.ntiles - i0, p.split_tiles);   // tiles of this part
     const int halves = k.nrows > kTile ? 2 : 1;         // row tiles in use
 
+    if (smem_u32(base) & 1023u) {       // the copies' swizzle counts on it
+        if (threadIdx.x == 0)
+            atomicOr(p.status, kStatusWait);
+        return;
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
             bar_init(&sh.raw[i], Q4 ? 128 : 1);
@@ -325,10 +321,10 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         }
         for (int i = 0; i < 4; ++i)
             bar_init(&sh.land[i], 1);
-        bar_init(&sh.q_full, 256);
+        bar_init(&sh.q_full, 32 * kSoftWarps);
         for (int i = 0; i < 2; ++i) {
             bar_init(&sh.s_full[i], 1);
-            bar_init(&sh.p_full[i], 128);
+            bar_init(&sh.p_full[i], 16 * kSoftWarps);
             bar_init(&sh.o_full[i], 1);
         }
         bar_init(&sh.drain, 1);
@@ -336,7 +332,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         sh.poison = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 8) {
+    if (warp == kSoftWarps) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&sh.tmem)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -347,33 +343,43 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     const uint32_t tmem = sh.tmem;
     const uint32_t tm_s[2] = {tmem, tmem + 128}, tm_o[2] = {tmem + 256, tmem + 256 + DP};
 
-    if (warp < 8) {
-        regs_up<Q4 ? 184 : 216>();
-        // ================================================ softmax, one row a thread
-        const int h = warp >> 2;                       // row tile
-        const int r = h * kTile + (warp & 3) * 32 + lane;
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // lane offset of the warp: 32 << 16
+    if (warp < kSoftWarps) {
+        regs_up<Q4 ? 88 : 104>();
+        // ================================================ softmax: half a row a thread
+        const int h = warp >> 3, q = warp >> 2 & 1, w4 = warp & 3;   // row tile, half, 32 rows
+        const int r_warp = h * kTile + w4 * 32, r = r_warp + lane;
+        const uint32_t lanes = (uint32_t)w4 << 21;                   // lane offset: 32 w4 << 16
+        const uint32_t s_mine = tm_s[h] + lanes + 64 * q;            // the half's scores, then weights
         const bool live = r < k.nrows;
         const int pos = live ? k.L - k.n + (k.row0 + r) / p.G : -1;
-        // The warp's 32 rows of Q into the K-major tile, whole rows at a time (a
-        // thread to a row costs 32 cache lines an instruction: 9 us a block); a
-        // negative scale goes into Q's signs.
-        constexpr int CH = DP / 8, AT_ONCE = 32 / CH;   // 16-byte chunks of a row, rows at once
-        const int r_warp = r - lane, ch = lane % CH;
+        // 16-byte chunks of a row of Q, and the rows a warp takes at once; where row
+        // r_warp + lane starts in q
+        constexpr int CH = DP / 8, AT_ONCE = 32 / CH;
+        int64_t q_off = 0;
+        if (live) {
+            int64_t t;
+            int qh;
+            attn_row_of(p, k, kvh, r, &t, &qh);
+            q_off = t * p.q_ts + qh * p.q_hs;
+        }
+        // 16 rows of Q into the K-major tile, whole rows at a time (a thread to a row
+        // costs 32 cache lines an instruction); a negative scale goes into Q's signs
         {
+            const int ch = lane % CH;
             const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-            constexpr int N = 32 / AT_ONCE;
+            constexpr int N = 16 / AT_ONCE;
             uint4 v[N];
-            RowWalk at(p, k, kvh, r_warp + lane / CH);
 #pragma unroll
-            for (int i = 0; i < N; ++i, at.step(AT_ONCE)) {
+            for (int i = 0; i < N; ++i) {
+                const int rl = 16 * q + i * AT_ONCE + lane / CH;
+                const int64_t off = __shfl_sync(0xffffffffu, q_off, rl);
                 v[i] = make_uint4(0, 0, 0, 0);
-                if (at.r < k.nrows && 8 * ch < p.c.D)
-                    v[i] = ld_stream(p.q + at.t * p.q_ts + at.h * p.q_hs + 8 * ch);
+                if (r_warp + rl < k.nrows && 8 * ch < p.c.D)
+                    v[i] = ld_stream(p.q + off + 8 * ch);
             }
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int row = (r_warp + i * AT_ONCE + lane / CH) & (kTile - 1);
+                const int row = w4 * 32 + 16 * q + i * AT_ONCE + lane / CH;
                 v[i].x ^= flip;
                 v[i].y ^= flip;
                 v[i].z ^= flip;
@@ -388,16 +394,17 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         }
         const float scale = fabsf(p.scale_log2);
         const int lo_r = p.window ? pos - p.window + 1 : 0;
-        float m = -INFINITY, l = 0.f;
-        bool ok = true;
+        float m = -INFINITY, l = 0.f;       // m is the same in both halves of a row
+        // the two warps of the same rows; neither ever leaves the loop alone
+        auto pair_sync = [&] {
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + h * 4 + w4) : "memory");
+        };
         if (h < halves) {
-            for (int j = 0; j < nt && ok; ++j) {
+            for (int j = 0; j < nt; ++j) {
                 const int j0 = k.tile_at(i0 + j) * kTile;
-                ok = bar_wait(&sh.s_full[h], j & 1, &sh.abort);
-                if (!ok)
-                    break;
+                bar_wait(&sh.s_full[h], j & 1, &sh.abort);
                 tc_fence_after();
-                uint32_t pk[kTile / 2];     // the weights, bf16 pairs
+                uint32_t pk[32];            // the weights, bf16 pairs
                 float sum = 0.f;
                 const bool full = attn_all_see(p, k, j0, kTile);
                 bool again = !full || j == 0;
@@ -408,37 +415,42 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                     float mx = -INFINITY;
                     uint64_t sum2[2] = {0, 0};
                     const uint64_t sc2 = pack_f2(scale, scale), rf2 = pack_f2(-m, -m);
-                    uint32_t s[2][32];
-                    tm_load32(s[0], tm_s[h] + lanes);
+                    uint32_t s[2][16];
+                    tm_load16(s[0], s_mine);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         tm_wait_load();
                         if (c < 3)
-                            tm_load32(s[(c + 1) & 1], tm_s[h] + lanes + 32 * (c + 1));
+                            tm_load16(s[(c + 1) & 1], s_mine + 16 * (c + 1));
                         const uint32_t *v = s[c & 1];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
+                        for (int e = 0; e < 16; e += 2) {
                             mx = max3_nan(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
                             uint64_t x = fma_f2(pack_u2(v[e], v[e + 1]), sc2, rf2);
                             // every kPolyEvery-th pair on the FMA pipe
                             x = (e / 2) % kPolyEvery == kPolyEvery - 1 ? exp2_poly2(x) : exp2_mufu2(x);
                             sum2[(e >> 1) & 1] = add_f2(sum2[(e >> 1) & 1], x);
-                            pk[16 * c + e / 2] = pack_bf2(x);
+                            pk[8 * c + e / 2] = pack_bf2(x);
                         }
                     }
                     const uint64_t both = add_f2(sum2[0], sum2[1]);
                     sum = f2_lo(both) + f2_hi(both);
-                    again = __any_sync(0xffffffffu, !(mx * scale <= m + kSlack));
+                    const bool bad = __any_sync(0xffffffffu, !(mx * scale <= m + kSlack));
+                    if (lane == 0)
+                        sh.over[j & 1][warp] = bad;
+                    pair_sync();
+                    again = bad || sh.over[j & 1][warp ^ 4];
                 }
                 if (again) {
-                    const int hi_c = pos - j0, lo_c = lo_r - j0, sink_c = p.n_sink - j0;
+                    const int hi_c = pos - j0 - 64 * q, lo_c = lo_r - j0 - 64 * q;
+                    const int sink_c = p.n_sink - j0 - 64 * q;
                     auto load = [&](uint32_t *v, int c) {
-                        tm_load32(v, tm_s[h] + lanes + 32 * c);
+                        tm_load16(v, s_mine + 16 * c);
                         tm_wait_load();
                         if (!full) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int t = 32 * c + e;
+                            for (int e = 0; e < 16; ++e) {
+                                const int t = 16 * c + e;
                                 if (!(t <= hi_c && (t >= lo_c || t < sink_c)))
                                     v[e] = 0xff800000u;
                             }
@@ -447,13 +459,17 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                     float mx = -INFINITY;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
+                        uint32_t v[16];
                         load(v, c);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
+                        for (int e = 0; e < 16; ++e)
                             mx = fmaxf(mx, __uint_as_float(v[e]));
                     }
-                    mx *= scale;
+                    // the row's maximum from both halves
+                    sh.half[h][q][w4 * 32 + lane] = mx;
+                    pair_sync();
+                    mx = fmaxf(mx, sh.half[h][q ^ 1][w4 * 32 + lane]) * scale;
+                    pair_sync();
                     if (__any_sync(0xffffffffu, mx > m + kSlack)) {
                         const float mn = fmaxf(m, mx);
                         const float f = m == -INFINITY ? 0.f : exp2_fast(m - mn);
@@ -462,13 +478,14 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                         if (j) {
 #pragma unroll
                             for (int c = 0; c < DP / 32; ++c) {
-                                uint32_t o[32];
-                                tm_load32(o, tm_o[h] + lanes + 32 * c);
+                                const uint32_t at = tm_o[h] + lanes + q * (DP / 2) + 16 * c;
+                                uint32_t o[16];
+                                tm_load16(o, at);
                                 tm_wait_load();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
+                                for (int e = 0; e < 16; ++e)
                                     o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tm_store32(tm_o[h] + lanes + 32 * c, o);
+                                tm_store16(at, o);
                             }
                         }
                     }
@@ -476,137 +493,142 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                     sum = 0.f;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
+                        uint32_t v[16];
                         load(v, c);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
+                        for (int e = 0; e < 16; e += 2) {
                             const float a = exp2_fast(fmaf(__uint_as_float(v[e]), scale, -ref));
                             const float b = exp2_fast(fmaf(__uint_as_float(v[e + 1]), scale, -ref));
                             sum += a + b;
-                            pk[16 * c + e / 2] = pack2(a, b);
+                            pk[8 * c + e / 2] = pack2(a, b);
                         }
                     }
                 }
                 l += sum;
-                tm_store32(tm_s[h] + lanes, pk);
-                tm_store32(tm_s[h] + lanes + 32, pk + 32);
+                tm_store32(s_mine, pk);
                 tm_wait_store();
                 tc_fence_before();
                 bar_arrive(&sh.p_full[h]);
             }
-            if (nt > 0 && ok)
-                ok = bar_wait(&sh.o_full[h], 0, &sh.abort);
+            if (nt > 0)
+                bar_wait(&sh.o_full[h], 0, &sh.abort);
             tc_fence_after();
             const bool only = nparts == 1;
-            const bool poison = *reinterpret_cast<volatile int *>(&sh.poison) != 0;
-            if (poison) {
-                for (int rr = r - lane; rr < min(r - lane + 32, k.nrows); ++rr) {
+            // both halves' sums, and one decision for both
+            sh.half[h][q][w4 * 32 + lane] = l;
+            if (lane == 0)
+                sh.sick[warp] = *reinterpret_cast<volatile int *>(&sh.poison);
+            pair_sync();
+            l += sh.half[h][q ^ 1][w4 * 32 + lane];
+            if (sh.sick[warp] | sh.sick[warp ^ 4]) {
+                for (int rr = r_warp + 16 * q; rr < min(r_warp + 16 * q + 16, k.nrows); ++rr) {
                     float pm, pl, po[E];
                     attn_row_exact<DP, Q4>(p, k, kvh, rr, i0, i0 + nt, &pm, &pl, po);
                     attn_emit<E>(p, k, kvh, rr, part, only, pm, pl, po);
                 }
             } else {
-                // O through shared memory (Q's tile is free), so that whole rows are
-                // written at a time: 64 dims in fp32 or all in bf16, the warp's rows
+                int64_t t = 0, row = 0;
+                int qh = 0;
+                if (live) {
+                    attn_row_of(p, k, kvh, r, &t, &qh);
+                    row = t * p.Hq + qh;
+                }
                 const bool empty = pos < 0;
                 const float inv = empty ? 0.f : 1.f / l;
-                uint8_t *slab = base + h * Lay::kStageBytes + (r_warp & (kTile - 1)) * (Lay::kHalves * 128);
+                const int64_t off = only ? t * p.o_ts + (int64_t)qh * p.c.D
+                                         : ((int64_t)part * p.T * p.Hq + row) * p.c.D;
+                // Half of O (DP/2 dims) through the warp's share of Q's tile, so that
+                // whole rows are written: bf16 at once, fp32 32 dims at a time.
+                constexpr int HD = DP / 2;
+                uint8_t *slab = base + (warp * (Lay::kQBytes / kSoftWarps));
                 if (only) {
-                    constexpr int ROW = Lay::kHalves * 128;
+                    constexpr int ROW = HD * 2, RC = ROW / 16;   // bytes, chunks
 #pragma unroll
-                    for (int c = 0; c < DP / 32; ++c) {
-                        uint32_t o[32];
+                    for (int c = 0; c < HD / 16; ++c) {
+                        uint32_t o[16];
                         if (nt > 0) {
-                            tm_load32(o, tm_o[h] + lanes + 32 * c);
+                            tm_load16(o, tm_o[h] + lanes + q * HD + 16 * c);
                             tm_wait_load();
                         }
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
+                        for (int g = 0; g < 2; ++g) {
                             float f[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 const int at = Q4 ? (e < 4 ? 2 * e : 2 * e - 7) : e;
                                 f[e] = nt == 0 || empty ? 0.f : __uint_as_float(o[8 * g + at]) * inv;
                             }
-                            const int x = 4 * c + g;
-                            *reinterpret_cast<uint4 *>(slab + lane * ROW + (x >> 3) * 128 +
-                                                       (((x & 7) ^ (lane & 7)) << 4)) = pack8(f);
+                            *reinterpret_cast<uint4 *>(slab + lane * ROW +
+                                                       (((2 * c + g) ^ (lane & (RC - 1))) << 4)) =
+                                pack8(f);
                         }
                     }
                     __syncwarp();
-                    RowWalk at(p, k, kvh, r_warp + lane / CH);
-                    constexpr int N = 8;        // rows a lane has in flight
-                    for (int i0 = 0; i0 < 32; i0 += N * AT_ONCE) {
-                        uint4 v[N];
+                    const int ch = lane % RC, d = q * HD + 8 * ch;
+                    constexpr int N = RC;       // 32 / RC rows at once
+                    uint4 v[N];
 #pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            const int rl = i0 + i * AT_ONCE + lane / CH;
-                            v[i] = *reinterpret_cast<const uint4 *>(
-                                slab + rl * ROW + (ch >> 3) * 128 + (((ch & 7) ^ (rl & 7)) << 4));
-                        }
+                    for (int i = 0; i < N; ++i) {
+                        const int rl = i * (32 / RC) + lane / RC;
+                        v[i] = *reinterpret_cast<const uint4 *>(slab + rl * ROW +
+                                                                ((ch ^ (rl & (RC - 1))) << 4));
+                    }
 #pragma unroll
-                        for (int i = 0; i < N; ++i, at.step(AT_ONCE))
-                            if (at.r < k.nrows && 8 * ch < p.c.D)
-                                *reinterpret_cast<uint4 *>(p.out + at.t * p.o_ts +
-                                                           (int64_t)at.h * p.c.D + 8 * ch) = v[i];
+                    for (int i = 0; i < N; ++i) {
+                        const int rl = i * (32 / RC) + lane / RC;
+                        const int64_t to = __shfl_sync(0xffffffffu, off, rl);
+                        if (r_warp + rl < k.nrows && d < p.c.D)
+                            *reinterpret_cast<uint4 *>(p.out + to + d) = v[i];
                     }
                 } else {
-                    // 32 dims of fp32 at a time: 128-byte rows, 8 lanes each
 #pragma unroll
-                    for (int c = 0; c < DP / 32; ++c) {
-                        uint32_t o[32];
+                    for (int c = 0; c < HD / 16; ++c) {
+                        uint32_t o[16];
                         if (nt > 0) {
-                            tm_load32(o, tm_o[h] + lanes + 32 * c);
+                            tm_load16(o, tm_o[h] + lanes + q * HD + 16 * c);
                             tm_wait_load();
                         }
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
+                        for (int g = 0; g < 2; ++g) {
                             uint32_t f[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 const int at = Q4 ? (e < 4 ? 2 * e : 2 * e - 7) : e;
                                 f[e] = nt == 0 ? 0u : o[8 * g + at];
                             }
-                            uint8_t *d = slab + lane * 128;
-                            *reinterpret_cast<uint4 *>(d + (((2 * g) ^ (lane & 7)) << 4)) =
+                            // 64-byte rows, two keys a 128-byte line
+                            uint8_t *to = slab + lane * 64;
+                            const int turn = lane >> 1 & 3;
+                            *reinterpret_cast<uint4 *>(to + (((2 * g) ^ turn) << 4)) =
                                 make_uint4(f[0], f[1], f[2], f[3]);
-                            *reinterpret_cast<uint4 *>(d + (((2 * g + 1) ^ (lane & 7)) << 4)) =
+                            *reinterpret_cast<uint4 *>(to + (((2 * g + 1) ^ turn) << 4)) =
                                 make_uint4(f[4], f[5], f[6], f[7]);
                         }
                         __syncwarp();
-                        RowWalk at(p, k, kvh, r_warp + lane / 8);
-                        uint4 v[8];
+                        const int ch = lane & 3, d = q * HD + 16 * c + 4 * ch;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int rl = 4 * i + lane / 8;
-                            v[i] = *reinterpret_cast<const uint4 *>(
-                                slab + rl * 128 + (((lane & 7) ^ (rl & 7)) << 4));
+                        for (int i = 0; i < 4; ++i) {
+                            const int rl = 8 * i + lane / 4;
+                            const int64_t to = __shfl_sync(0xffffffffu, off, rl);
+                            const uint4 v = *reinterpret_cast<const uint4 *>(
+                                slab + rl * 64 + ((ch ^ (rl >> 1 & 3)) << 4));
+                            if (r_warp + rl < k.nrows && d < p.c.D)
+                                *reinterpret_cast<uint4 *>(p.ws_o + to + d) = v;
                         }
-                        const int d = 32 * c + 4 * (lane & 7);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i, at.step(4))
-                            if (at.r < k.nrows && d < p.c.D) {
-                                const int64_t row = ((int64_t)part * p.T + at.t) * p.Hq + at.h;
-                                *reinterpret_cast<uint4 *>(p.ws_o + row * p.c.D + d) = v[i];
-                            }
                         __syncwarp();
                     }
                 }
-                if (live && (!only || p.lse)) {
-                    int64_t t;
-                    int qh;
-                    attn_row_of(p, k, kvh, r, &t, &qh);
+                if (live && q == 0) {
                     if (!only)
-                        p.ws_ml[((int64_t)part * p.T + t) * p.Hq + qh] = make_float2(m, l);
-                    else
-                        p.lse[t * p.Hq + qh] =
-                            empty ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+                        p.ws_ml[(int64_t)part * p.T * p.Hq + row] = make_float2(m, l);
+                    else if (p.lse)
+                        p.lse[row] = empty ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
                 }
             }
         }
     } else {
-    regs_down<72>();
-    if (warp == 8) {
+    regs_down<64>();
+    if (warp == kSoftWarps) {
         // ================================================ matrix instructions
         constexpr uint32_t kId = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(kTile / 16) << 24;
         constexpr uint32_t kIdS = kId | (uint32_t)(kTile / 8) << 17;
@@ -642,7 +664,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                     const uint64_t b = dv + sv * kStage16;
 #pragma unroll
                     for (int s = 0; s < kTile / 16; ++s)
-                        mma_ts(o_at, s_at + 8 * s, b + s * 128, kIdO, j > 0 || s > 0);
+                        mma_ts(o_at, s_at + 64 * (s >> 2) + 8 * (s & 3), b + s * 128, kIdO, j > 0 || s > 0);
                     if (!next)
                         tc_commit(&sh.o_full[h]);
                 }
@@ -676,7 +698,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         // everything issued has finished, whatever became of the rest
         for (uint32_t i = 0; i < kWaitLimit && !__all_sync(0xffffffffu, bar_try(&sh.drain, 0)); ++i) {
         }
-    } else if (!Q4 && warp == 9) {
+    } else if (!Q4 && warp == kSoftWarps + 1) {
         // ================================================ TMA
         // A lane looks up one run of `box` keys of a tile, once for K and V, and
         // asks for the next tile's before it waits.
@@ -740,7 +762,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                 }
         }
         __syncwarp();
-    } else if (!Q4 && (warp == 10 || warp == 11)) {
+    } else if (!Q4 && warp >= kSoftWarps + 2) {
         // ================================================ values no row, or not every row, sees
         // the two warps take such tiles in turn
         const bool mixed = k.p_first != k.p_last;
@@ -750,7 +772,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             if (attn_all_see(p, k, j0, kTile))
                 continue;
             const int e = edges++;
-            if ((e & 1) != warp - 10)
+            if ((e & 1) != warp - (kSoftWarps + 2))
                 continue;
             const int st = (2 * j + 1) % NST;
             if (!bar_wait(&sh.land[e & 3], (e >> 2) & 1, &sh.abort))
@@ -793,9 +815,9 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             if (lane == 0)
                 bar_arrive(&sh.raw[st]);
         }
-    } else if (Q4 && warp >= 12) {
+    } else if (Q4 && warp >= kSoftWarps + 4) {
         // ================================================ 4 bits to bf16, one key a thread
-        const int row = threadIdx.x - 384;
+        const int row = threadIdx.x - 32 * (kSoftWarps + 4);
         constexpr int GR = DP / 32;
         uint32_t code[4 * GR], sc[GR / 2];
         auto fetch = [&](int it) {
@@ -889,7 +911,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kSoftWarps) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
     }
@@ -905,7 +927,7 @@ cudaError_t tiles_launch(const AttnParams &p, const CacheMaps &map, cudaStream_t
     if (e != cudaSuccess)
         return e;
     const dim3 grid((unsigned)(p.n_blocks * p.c.Hkv * p.nsplit));
-    return launch(fn, grid, dim3(Q4 ? 512 : 384), Layout<DP>::kBytes, stream, 1, p, map);
+    return launch(fn, grid, dim3(tiles_threads(Q4)), Layout<DP>::kBytes, stream, 1, p, map);
 }
 
 }  // namespace
@@ -925,7 +947,7 @@ cudaError_t launch_attn_tiles(const AttnParams &p, int q4, cudaStream_t stream, 
     }
     if (e == cudaSuccess && rec) {
         rec->kernel = QKR_KERNEL_ATTN_TILES;
-        rec->block = q4 ? 512 : 384;
+        rec->block = tiles_threads(q4 != 0);
         rec->grid = p.n_blocks * p.c.Hkv * p.nsplit;
         rec->stages = p.nsplit;
         rec->heads_per_item = p.rows;
