@@ -63,7 +63,10 @@ namespace {
 
 constexpr int kWarps = 4;              // computing warps; one more feeds them
 constexpr int kThreads = 32 * (kWarps + 1);
-constexpr uint32_t kWaitLimit = 1u << 21;
+// A wait asks the hardware to sleep up to kWaitHint ns, kWaitLimit times at most.
+// (Without the hint it returns after some 50 clocks: the polls were a quarter of
+// all instructions.)
+constexpr uint32_t kWaitHint = 100000, kWaitLimit = 1u << 14;
 constexpr uint32_t kMinus136 = 0xc308c308u;  // bf16 pair
 constexpr float kSlack = 8.f;  // log2 units the reference may lag behind the maximum
 
@@ -171,9 +174,9 @@ __device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity)
     uint32_t ok;
     asm volatile(
         "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
         " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok) : "r"(sm_u32(bar)), "r"(parity) : "memory");
+        : "=r"(ok) : "r"(sm_u32(bar)), "r"(parity), "r"(kWaitHint) : "memory");
     return ok != 0;
 }
 // Bounded; after a wait that ran out no other waits (the result is reported as
@@ -183,7 +186,7 @@ __device__ __noinline__ void bar_wait_long(uint64_t *bar, uint32_t parity, int *
     for (uint32_t i = 0; i < kWaitLimit; ++i) {
         if (bar_try(bar, parity))
             return;
-        if ((i & 15u) == 15u && *reinterpret_cast<volatile int *>(abort))
+        if (*reinterpret_cast<volatile int *>(abort))
             return;
     }
     *reinterpret_cast<volatile int *>(abort) = 1;

@@ -55,11 +55,14 @@ constexpr int kSoftWarps = 16;
 constexpr int tiles_threads(bool q4) { return 32 * (kSoftWarps + (q4 ? 8 : 4)); }
 constexpr int kTile = 128;               // keys of a tile, rows of a tile
 constexpr float kSlack = 8.f;
-constexpr int kPolyEvery = 4;
+constexpr int kPolyEvery = 8;
 constexpr float kExpC0 = 0.9999992847442627f, kExpC1 = 0.6931217908859253f,
                 kExpC2 = 0.240247443318367f, kExpC3 = 0.05591785907745361f,
                 kExpC4 = 0.009570100344717503f;
-constexpr uint32_t kWaitLimit = 1u << 21;
+// A wait asks the hardware to sleep up to kWaitHint ns, kWaitLimit times at most.
+// (Without the hint it returns after some 50 clocks: the polls were a quarter of
+// all instructions.)
+constexpr uint32_t kWaitHint = 100000, kWaitLimit = 1u << 14;
 
 struct Shared {
     uint64_t raw[8], empty[8];            // ring: full, free
@@ -104,9 +107,9 @@ __device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity)
     uint32_t ok;
     asm volatile(
         "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
         " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
+        : "=r"(ok) : "r"(smem_u32(b)), "r"(parity), "r"(kWaitHint) : "memory");
     return ok != 0;
 }
 // By a whole warp.  False when the wait ran out or another role's has.
@@ -115,7 +118,7 @@ __device__ __forceinline__ bool bar_wait_long(uint64_t *b, uint32_t parity, int 
     for (uint32_t i = 0; i < kWaitLimit; ++i) {
         if (bar_try(b, parity))
             return true;
-        if ((i & 15u) == 15u && *reinterpret_cast<volatile int *>(abort))
+        if (*reinterpret_cast<volatile int *>(abort))
             return false;
     }
     *reinterpret_cast<volatile int *>(abort) = 1;
@@ -166,18 +169,37 @@ __device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t addr)
     return base | (uint64_t)((addr >> 4) & 0x3fffu);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int acc)
+// One product of a tile, 16 of the summed dimension an instruction.  S: operands
+// in shared memory, 2 descriptor units (32 bytes) a step, the next 64 dims half a
+// tile on.  O: the weights from tensor memory (8 columns a step, the second half
+// 64 columns on), V 16 keys (2048 bytes) a step.
+#define QKR_MMA_P "tcgen05.mma.cta_group::1.kind::f16 "
+#define QKR_SS(o) " add.s64 a, %1, " #o ";\n add.s64 b, %2, " #o ";\n @e " QKR_MMA_P "[%0], a, b, %3, t;\n"
+#define QKR_TS(o, v) " add.s32 a, %1, " #o ";\n add.s64 b, %2, " #v ";\n @e " QKR_MMA_P "[%0], [a], b, %3, t;\n"
+template <int DP>
+__device__ __forceinline__ void product_s(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc)
 {
-    asm volatile(
-        "{\n .reg .pred p, e;\n setp.ne.u32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+    if constexpr (DP == 128)
+        asm volatile(
+            "{\n .reg .pred e, t, f;\n .reg .b64 a, b;\n elect.sync _|e, 0xffffffff;\n"
+            " setp.eq.u32 t, %3, %3;\n setp.ne.u32 f, %3, %3;\n"
+            " @e " QKR_MMA_P "[%0], %1, %2, %3, f;\n" QKR_SS(2) QKR_SS(4) QKR_SS(6) QKR_SS(1024)
+                QKR_SS(1026) QKR_SS(1028) QKR_SS(1030) "}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc) : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred e, t, f;\n .reg .b64 a, b;\n elect.sync _|e, 0xffffffff;\n"
+            " setp.eq.u32 t, %3, %3;\n setp.ne.u32 f, %3, %3;\n"
+            " @e " QKR_MMA_P "[%0], %1, %2, %3, f;\n" QKR_SS(2) QKR_SS(4) QKR_SS(6) "}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int acc)
+__device__ __forceinline__ void product_o(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int acc)
 {
     asm volatile(
-        "{\n .reg .pred p, e;\n setp.ne.u32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+        "{\n .reg .pred e, t, f;\n .reg .b32 a;\n .reg .b64 b;\n elect.sync _|e, 0xffffffff;\n"
+        " setp.eq.u32 t, %3, %3;\n setp.ne.u32 f, %4, 0;\n"
+        " @e " QKR_MMA_P "[%0], [%1], %2, %3, f;\n" QKR_TS(8, 128) QKR_TS(16, 256) QKR_TS(24, 384)
+            QKR_TS(64, 512) QKR_TS(72, 640) QKR_TS(80, 768) QKR_TS(88, 896) "}"
         ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
 
@@ -661,10 +683,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                     if (!ok)
                         break;
                     tc_fence_after();
-                    const uint64_t b = dv + sv * kStage16;
-#pragma unroll
-                    for (int s = 0; s < kTile / 16; ++s)
-                        mma_ts(o_at, s_at + 64 * (s >> 2) + 8 * (s & 3), b + s * 128, kIdO, j > 0 || s > 0);
+                    product_o(o_at, s_at, dv + sv * kStage16, kIdO, j > 0);
                     if (!next)
                         tc_commit(&sh.o_full[h]);
                 }
@@ -674,12 +693,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                     if (!ok)
                         break;
                     tc_fence_after();
-                    const uint64_t a = dq + h * kStage16, b = dk + sk * kStage16;
-#pragma unroll
-                    for (int s = 0; s < DP / 16; ++s) {
-                        const uint32_t off = (s >> 2) * (kTile * 8) + (s & 3) * 2;
-                        mma_ss(s_at, a + off, b + off, kIdS, s > 0);
-                    }
+                    product_s<DP>(s_at, dq + h * kStage16, dk + sk * kStage16, kIdS);
                     tc_commit(&sh.s_full[h]);
                 }
             }
