@@ -802,10 +802,10 @@ attn_cluster_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     pdl_trigger();
     cg::cluster_group cluster = cg::this_cluster();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int size = p.cluster, rank = (int)(blockIdx.x % size);
-    const int item = (int)(blockIdx.x / size);
-    const int kvh = item % p.c.Hkv;
-    const AttnBlock k = attn_block(p, item / p.c.Hkv);
+    const int size = p.cluster, rank = (int)(blockIdx.x % (uint32_t)size);
+    const uint32_t item = blockIdx.x / (uint32_t)size;
+    const int kvh = (int)(item % (uint32_t)p.c.Hkv);
+    const AttnBlock k = attn_block(p, item / (uint32_t)p.c.Hkv);
     if (k.b < 0)
         return;     // the whole cluster
     const int share = (k.ntiles + size - 1) / size;
@@ -1031,10 +1031,11 @@ attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
         atomicOr(p.status, kStatusWait);
 }
 
-// Joins the pieces of the block that CTA x / rows began, row x % rows.
+// Joins the pieces of the block that CTA x / used began, row x % used (`used`: the
+// most rows a block of this launch has).
 template <int DP>
 __global__ void __launch_bounds__(32 * kWarps)
-attn_rows_join_kernel(const __grid_constant__ AttnParams p)
+attn_rows_join_kernel(const __grid_constant__ AttnParams p, int used)
 {
     constexpr int E = DP / 32;
     __shared__ float sm_o[kWarps][DP];
@@ -1042,7 +1043,7 @@ attn_rows_join_kernel(const __grid_constant__ AttnParams p)
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int cta = (int)(blockIdx.x / p.rows), r = (int)(blockIdx.x % p.rows);
+    const int cta = (int)(blockIdx.x / (uint32_t)used), r = (int)(blockIdx.x % (uint32_t)used);
     const AttnSpan s = p.ws_span[cta];
     if (s.b < 0 || r >= s.n * p.G)
         return;
@@ -1101,74 +1102,59 @@ attn_rows_join_kernel(const __grid_constant__ AttnParams p)
     attn_emit<E>(p, k, s.kvh, r, 0, true, m, l, acc);
 }
 
-// Joins the parts of a row: one CTA per block row and KV head; the warps take
-// every fourth part.
+// Joins the parts of the tiles kernel: a CTA takes 64 rows of a block, a warp a
+// row at a time (a row has few parts, each D consecutive numbers).
+constexpr int kJoinRows = 64, kJoinWarps = 8;
 template <int DP>
-__global__ void __launch_bounds__(32 * kWarps) attn_join_kernel(const __grid_constant__ AttnParams p,
-                                                                int rows_used)
+__global__ void __launch_bounds__(32 * kJoinWarps)
+attn_join_kernel(const __grid_constant__ AttnParams p)
 {
     constexpr int E = DP / 32;
-    __shared__ float sm_o[kWarps][DP];
-    __shared__ float sm_l[kWarps], sm_m[kWarps];
     pdl_wait();
     pdl_trigger();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t x = blockIdx.x;
-    const int r = (int)(x % rows_used);
-    const int kvh = (int)(x / rows_used % p.c.Hkv);
-    const AttnBlock k = attn_block(p, x / rows_used / p.c.Hkv);
-    if (k.b < 0 || r >= k.nrows)
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = lane * E;
+    const uint32_t chunks = (p.rows + kJoinRows - 1) / kJoinRows, x = blockIdx.x;
+    const int r0 = (int)(x % chunks) * kJoinRows;
+    const int kvh = (int)(x / chunks % (uint32_t)p.c.Hkv);
+    const AttnBlock k = attn_block(p, x / chunks / (uint32_t)p.c.Hkv);
+    if (k.b < 0 || r0 >= k.nrows)
         return;
     const int nparts = max(1, (k.ntiles + p.split_tiles - 1) / p.split_tiles);
     if (nparts == 1)
         return;  // written already
-    int64_t t;
-    int h;
-    attn_row_of(p, k, kvh, r, &t, &h);
-    const int64_t row = t * p.Hq + h, step = p.T * p.Hq;
-    float m = -INFINITY;
-    for (int s = warp * 32 + lane; s < nparts; s += 32 * kWarps)
-        m = fmaxf(m, p.ws_ml[row + s * step].x);
+    const int64_t step = p.T * p.Hq;
+    for (int r = r0 + warp; r < min(k.nrows, r0 + kJoinRows); r += kJoinWarps) {
+        int64_t t;
+        int h;
+        attn_row_of(p, k, kvh, r, &t, &h);
+        const int64_t row = t * p.Hq + h;
+        float m = -INFINITY;
+        for (int s = lane; s < nparts; s += 32)
+            m = fmaxf(m, p.ws_ml[row + s * step].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0)
-        sm_m[warp] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
-    float l = 0.f, acc[E];
+        for (int o = 16; o > 0; o >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float l = 0.f, acc[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        acc[e] = 0.f;
-    const int d = lane * E;
+        for (int e = 0; e < E; ++e)
+            acc[e] = 0.f;
 #pragma unroll 4
-    for (int s = warp; s < nparts; s += kWarps) {
-        const float2 ml = p.ws_ml[row + s * step];
-        const float f = m == -INFINITY ? 0.f : exp2_fast(ml.x - m);
-        l += f * ml.y;
-        if (d < p.c.D) {
-            const float *w = p.ws_o + (row + s * step) * p.c.D + d;
+        for (int s = 0; s < nparts; ++s) {
+            const float2 ml = p.ws_ml[row + s * step];
+            const float f = m == -INFINITY ? 0.f : exp2_fast(ml.x - m);
+            l += f * ml.y;
+            if (d < p.c.D) {
+                const float *w = p.ws_o + (row + s * step) * p.c.D + d;
 #pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const float2 v = *reinterpret_cast<const float2 *>(w + e);
-                acc[e] += f * v.x;
-                acc[e + 1] += f * v.y;
+                for (int e = 0; e < E; e += 2) {
+                    const float2 v = *reinterpret_cast<const float2 *>(w + e);
+                    acc[e] += f * v.x;
+                    acc[e + 1] += f * v.y;
+                }
             }
         }
+        attn_emit<E>(p, k, kvh, r, 0, true, m, l, acc);
     }
-    if (lane == 0)
-        sm_l[warp] = l;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        sm_o[warp][d + e] = acc[e];
-    __syncthreads();
-    if (warp)
-        return;
-    l = ((sm_l[0] + sm_l[1]) + sm_l[2]) + sm_l[3];
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        acc[e] = ((sm_o[0][d + e] + sm_o[1][d + e]) + sm_o[2][d + e]) + sm_o[3][d + e];
-    attn_emit<E>(p, k, kvh, r, 0, true, m, l, acc);
 }
 
 template <int DP, int NT, bool Q4>
@@ -1188,8 +1174,10 @@ cudaError_t rows_launch(const AttnParams &p, cudaStream_t stream, LaunchRecord *
     e = launch(fn, dim3((unsigned)rec->grid), dim3(kThreads), smem, stream, rec->cluster, p,
                maps);
     if (e == cudaSuccess && p.ctas) {
-        e = launch(attn_rows_join_kernel<DP>, dim3((unsigned)(p.ctas * p.rows)), dim3(32 * kWarps), 0,
-                   stream, 1, p);
+        const int64_t most = (int64_t)p.max_q * p.G;
+        const int used = (int)(most < p.rows ? most : p.rows);
+        e = launch(attn_rows_join_kernel<DP>, dim3((unsigned)(p.ctas * used)), dim3(32 * kWarps), 0,
+                   stream, 1, p, used);
         rec->launches += 1;
     }
     return e;
@@ -1231,12 +1219,10 @@ cudaError_t launch_attn_rows(const AttnParams &p, int q4, cudaStream_t stream, L
 
 cudaError_t launch_attn_join(const AttnParams &p, cudaStream_t stream)
 {
-    const int64_t most = (int64_t)p.max_q * p.G;
-    const int used = (int)(most < p.rows ? most : p.rows);
-    const dim3 grid((unsigned)(p.n_blocks * p.c.Hkv * used));
-    return p.c.D <= 64 ? launch(attn_join_kernel<64>, grid, dim3(32 * kWarps), 0, stream, 1, p, used)
-                       : launch(attn_join_kernel<128>, grid, dim3(32 * kWarps), 0, stream, 1, p,
-                                used);
+    const int64_t chunks = (p.rows + kJoinRows - 1) / kJoinRows;
+    const dim3 grid((unsigned)(p.n_blocks * p.c.Hkv * chunks)), block(32 * kJoinWarps);
+    return p.c.D <= 64 ? launch(attn_join_kernel<64>, grid, block, 0, stream, 1, p)
+                       : launch(attn_join_kernel<128>, grid, block, 0, stream, 1, p);
 }
 
 }  // namespace qkr

@@ -45,6 +45,8 @@
 // all roles stop issuing, copies and matrix instructions in flight are waited
 // for (bounded), tensor memory is freed and the block ends.
 
+#include <type_traits>
+
 #include "cache_attn.cuh"
 #include "cache_tma.cuh"
 
@@ -274,12 +276,13 @@ __device__ __forceinline__ uint64_t exp2_mufu2(uint64_t x)
 // 2^x for x <= 2^7 on the FMA pipe: x = n + f with n the nearest integer (the
 // rounding of x + 1.5 * 2^23, whose low bits are n), 2^f by the polynomial of
 // degree 4 with the least relative error on [-1/2, 1/2] (Remez; 2.7e-6, a
-// thousandth of the bf16 rounding that follows), n added to the exponent.  x
-// below -126 counts as -126.
+// thousandth of the bf16 rounding that follows), n added to the exponent; 0
+// below x = -126, as the instruction gives.
 __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x)
 {
     const uint64_t big = pack_f2(12582912.f, 12582912.f), nbig = pack_f2(-12582912.f, -12582912.f);
-    x = pack_f2(fmaxf(f2_lo(x), -126.f), fmaxf(f2_hi(x), -126.f));
+    const float lo = f2_lo(x), hi = f2_hi(x);
+    x = pack_f2(fmaxf(lo, -126.f), fmaxf(hi, -126.f));
     const uint64_t t = add_f2(x, big);
     const uint64_t f = fma_f2(add_f2(t, nbig), pack_f2(-1.f, -1.f), x);
     uint64_t r = pack_f2(kExpC4, kExpC4);
@@ -287,7 +290,8 @@ __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x)
     r = fma_f2(r, f, pack_f2(kExpC2, kExpC2));
     r = fma_f2(r, f, pack_f2(kExpC1, kExpC1));
     r = fma_f2(r, f, pack_f2(kExpC0, kExpC0));
-    return pack_u2((uint32_t)r + ((uint32_t)t << 23), (uint32_t)(r >> 32) + ((uint32_t)(t >> 32) << 23));
+    return pack_u2(lo < -126.f ? 0u : (uint32_t)r + ((uint32_t)t << 23),
+                   hi < -126.f ? 0u : (uint32_t)(r >> 32) + ((uint32_t)(t >> 32) << 23));
 }
 
 template <int REGS>
@@ -315,21 +319,6 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     uint8_t *ring = base + Lay::kQBytes;
     Shared &sh = *reinterpret_cast<Shared *>(ring + NST * Lay::kStageBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-    pdl_wait();
-    pdl_trigger();
-    const int64_t x = blockIdx.x;
-    const int kvh = (int)(x % p.c.Hkv);
-    const int part = (int)(x / p.c.Hkv / p.n_blocks);
-    const AttnBlock k = attn_block(p, x / p.c.Hkv % p.n_blocks);
-    if (k.b < 0)
-        return;
-    const int nparts = max(1, (k.ntiles + p.split_tiles - 1) / p.split_tiles);
-    if (part >= nparts)
-        return;
-    const int i0 = part * p.split_tiles;
-    const int nt = min(k.ntiles - i0, p.split_tiles);   // tiles of this part
-    const int halves = k.nrows > kTile ? 2 : 1;         // row tiles in use
 
     if (smem_u32(base) & 1023u) {       // the copies' swizzle counts on it
         if (threadIdx.x == 0)
@@ -359,10 +348,27 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                          smem_u32(&sh.tmem)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
+    pdl_wait();
+    pdl_trigger();
+    const uint32_t x = blockIdx.x, Hkv = p.c.Hkv, rest = x / Hkv;
+    const int kvh = (int)(x % Hkv);
+    const int part = (int)(rest / (uint32_t)p.n_blocks);
+    const AttnBlock k = attn_block(p, rest % (uint32_t)p.n_blocks);
+    const int nparts = max(1, (k.ntiles + p.split_tiles - 1) / p.split_tiles);
+    const int i0 = part * p.split_tiles;
+    const int nt = min(k.ntiles - i0, p.split_tiles);   // tiles of this part
+    const int halves = k.nrows > kTile ? 2 : 1;         // row tiles in use
+
+    const bool used = k.b >= 0 && part < nparts;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
+    if (!used) {
+        if (warp == kSoftWarps)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+        return;
+    }
     const uint32_t tm_s[2] = {tmem, tmem + 128}, tm_o[2] = {tmem + 256, tmem + 256 + DP};
 
     if (warp < kSoftWarps) {
@@ -429,32 +435,57 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                 uint32_t pk[32];            // the weights, bf16 pairs
                 float sum = 0.f;
                 const bool full = attn_all_see(p, k, j0, kTile);
-                bool again = !full || j == 0;
+                // the keys 16c .. of the half that this row sees, a bit each
+                auto seen = [&](int c) -> uint32_t {
+                    auto below = [](int n) -> uint32_t {       // bits [0, n) of 16
+                        return (1u << min(max(n, 0), 16)) - 1u;
+                    };
+                    const int first = j0 + 64 * q + 16 * c;
+                    return full ? 0xffffu
+                                : below(pos + 1 - first) &
+                                      (~below(lo_r - first) | below(p.n_sink - first));
+                };
+                bool again = j == 0;
                 if (!again) {
                     // Against the reference as it stands, in one pass: where the
                     // maximum then turns out to exceed it by too much (or a score
                     // is NaN) the tile is done again below.
+                    const float ref = m == -INFINITY ? 0.f : m;
                     float mx = -INFINITY;
                     uint64_t sum2[2] = {0, 0};
-                    const uint64_t sc2 = pack_f2(scale, scale), rf2 = pack_f2(-m, -m);
+                    const uint64_t sc2 = pack_f2(scale, scale), rf2 = pack_f2(-ref, -ref);
                     uint32_t s[2][16];
-                    tm_load16(s[0], s_mine);
+                    auto pass = [&](auto masked) {
+                        tm_load16(s[0], s_mine);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tm_wait_load();
-                        if (c < 3)
-                            tm_load16(s[(c + 1) & 1], s_mine + 16 * (c + 1));
-                        const uint32_t *v = s[c & 1];
+                        for (int c = 0; c < 4; ++c) {
+                            tm_wait_load();
+                            if (c < 3)
+                                tm_load16(s[(c + 1) & 1], s_mine + 16 * (c + 1));
+                            uint32_t *v = s[c & 1];
+                            if constexpr (masked.value) {
+                                const uint32_t bits = seen(c);
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            mx = max3_nan(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-                            uint64_t x = fma_f2(pack_u2(v[e], v[e + 1]), sc2, rf2);
-                            // every kPolyEvery-th pair on the FMA pipe
-                            x = (e / 2) % kPolyEvery == kPolyEvery - 1 ? exp2_poly2(x) : exp2_mufu2(x);
-                            sum2[(e >> 1) & 1] = add_f2(sum2[(e >> 1) & 1], x);
-                            pk[8 * c + e / 2] = pack_bf2(x);
+                                for (int e = 0; e < 16; ++e)
+                                    if (!(bits >> e & 1u))
+                                        v[e] = 0xff800000u;
+                            }
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                mx = max3_nan(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                                uint64_t x = fma_f2(pack_u2(v[e], v[e + 1]), sc2, rf2);
+                                // every kPolyEvery-th pair on the FMA pipe
+                                x = !masked.value && (e / 2) % kPolyEvery == kPolyEvery - 1
+                                        ? exp2_poly2(x) : exp2_mufu2(x);
+                                sum2[(e >> 1) & 1] = add_f2(sum2[(e >> 1) & 1], x);
+                                pk[8 * c + e / 2] = pack_bf2(x);
+                            }
                         }
-                    }
+                    };
+                    if (full)
+                        pass(std::false_type{});
+                    else
+                        pass(std::true_type{});
                     const uint64_t both = add_f2(sum2[0], sum2[1]);
                     sum = f2_lo(both) + f2_hi(both);
                     const bool bad = __any_sync(0xffffffffu, !(mx * scale <= m + kSlack));
@@ -464,19 +495,14 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                     again = bad || sh.over[j & 1][warp ^ 4];
                 }
                 if (again) {
-                    const int hi_c = pos - j0 - 64 * q, lo_c = lo_r - j0 - 64 * q;
-                    const int sink_c = p.n_sink - j0 - 64 * q;
                     auto load = [&](uint32_t *v, int c) {
                         tm_load16(v, s_mine + 16 * c);
                         tm_wait_load();
-                        if (!full) {
+                        const uint32_t bits = seen(c);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const int t = 16 * c + e;
-                                if (!(t <= hi_c && (t >= lo_c || t < sink_c)))
-                                    v[e] = 0xff800000u;
-                            }
-                        }
+                        for (int e = 0; e < 16; ++e)
+                            if (!(bits >> e & 1u))
+                                v[e] = 0xff800000u;
                     };
                     float mx = -INFINITY;
 #pragma unroll

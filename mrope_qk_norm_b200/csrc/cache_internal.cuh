@@ -136,16 +136,16 @@ __device__ __forceinline__ AttnBlock attn_block_at(const AttnParams &p, int b, i
 // The block of block index `idx`, computed by a whole warp.  Where the blocks
 // are not laid out per sequence, each lane counts those of one sequence and
 // the warp adds them up, 32 sequences at a time.
-__device__ __forceinline__ AttnBlock attn_block(const AttnParams &p, int64_t idx)
+__device__ __forceinline__ AttnBlock attn_block(const AttnParams &p, uint32_t idx)
 {
-    AttnBlock none;
+    AttnBlock none = {};
     none.b = -1;
     int b = -1, blk = 0, nblk = 0, n_of = 0;
     int64_t t0_of = 0;
     bool bad = false;
     if (p.direct) {
-        b = (int)(idx / p.blocks_max);
-        blk = (int)(idx % p.blocks_max);
+        b = (int)(idx / (uint32_t)p.blocks_max);
+        blk = (int)(idx % (uint32_t)p.blocks_max);
         n_of = attn_seq(p, b, &t0_of, &bad);
         nblk = attn_blocks_of(p, n_of);
         if (blk >= nblk)
