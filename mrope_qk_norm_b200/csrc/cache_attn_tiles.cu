@@ -19,8 +19,8 @@
 //   warp 16         issues the matrix instructions, in the order
 //                   P0 V(j), Q0 K(j+1), P1 V(j), Q1 K(j+1): while one tile's
 //                   softmax runs, the tensor cores work for the other
-//   bf16: warp 17   K and V tiles by TMA, a ring of 32 KB (16 KB) stages
-//         18, 19    clear the values no row of the block sees (below)
+//   bf16: 17, 18    K tiles, V tiles by TMA, a ring of 32 KB (16 KB) stages
+//         19        clears the values no row of the block sees (below)
 //   4 bits: 20-23   K and V tiles from nibbles to bf16 in shared memory, one
 //                   key a thread
 //
@@ -738,10 +738,12 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         // everything issued has finished, whatever became of the rest
         for (uint32_t i = 0; i < kWaitLimit && !__all_sync(0xffffffffu, bar_try(&sh.drain, 0)); ++i) {
         }
-    } else if (!Q4 && warp == kSoftWarps + 1) {
-        // ================================================ TMA
-        // A lane looks up one run of `box` keys of a tile, once for K and V, and
-        // asks for the next tile's before it waits.
+    } else if (!Q4 && (warp == kSoftWarps + 1 || warp == kSoftWarps + 2)) {
+        // ================================================ TMA: one warp K, one V
+        // A lane looks up one run of `box` keys of a tile and asks for the next
+        // tile's before it waits.
+        const bool is_v = warp == kSoftWarps + 2;
+        const PlaneMap &map_of = is_v ? map.v : map.k;
         const int box = map.k.box, copies = kTile / box, c = lane * box;
         const bool mine = lane < copies;
         auto look = [&](int j, int *page, int *row) {
@@ -757,25 +759,22 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         int page, row, page_next, row_next;
         look(0, &page, &row);
         bool ok = true;
-        int it = 0, edges = 0;
-        for (; it < 2 * nt; ++it) {
-            const int st = it % NST;
-            const bool is_v = it & 1;
-            if (!is_v)
-                look((it >> 1) + 1, &page_next, &row_next);
+        int j = 0, edges = 0;
+        for (; j < nt; ++j) {
+            const int it = 2 * j + is_v, st = it % NST;
+            look(j + 1, &page_next, &row_next);
             if (it >= NST)
                 ok = bar_wait(&sh.empty[st], (it / NST - 1) & 1, &sh.abort);
             if (!ok)
                 break;
             // the values of a tile that not every row sees go past a clearing warp
             uint64_t *bar = &sh.raw[st];
-            if (is_v && !attn_all_see(p, k, k.tile_at(i0 + (it >> 1)) * kTile, kTile))
+            if (is_v && !attn_all_see(p, k, k.tile_at(i0 + j) * kTile, kTile))
                 bar = &sh.land[edges++ & 3];
             if (lane == 0)
                 bar_expect(bar, Lay::kStageBytes);
             __syncwarp();
             const uint32_t stage = smem_u32(ring) + st * Lay::kStageBytes;
-            const PlaneMap &map_of = is_v ? map.v : map.k;
             int c1, c2, c3;
             plane_coords(map_of, row, kvh, page, &c1, &c2, &c3);
 #pragma unroll 2
@@ -787,24 +786,24 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                     plane_copy(map_of, stage + hf * (kTile * 128) + x * (box * 128), smem_u32(bar),
                                64 * hf, a1, a2, a3);
             }
-            if (is_v) {
-                page = page_next;
-                row = row_next;
-            }
+            page = page_next;
+            row = row_next;
         }
-        // no copy is left in flight
+        // no copy is left in flight (the ring's last stages, this warp's of them)
         if (lane == 0) {
-            for (int i = it > NST ? it - NST : 0; i < it; ++i)
-                for (uint32_t n = 0; n < kWaitLimit && !bar_try(&sh.raw[i % NST], (i / NST) & 1); ++n) {
-                }
+            for (int y = max(0, j - NST / 2 - 1); y < j; ++y) {
+                const int it = 2 * y + is_v;
+                if (it + NST >= 2 * j + is_v)
+                    for (uint32_t n = 0; n < kWaitLimit && !bar_try(&sh.raw[it % NST], (it / NST) & 1); ++n) {
+                    }
+            }
             for (int i = edges > 4 ? edges - 4 : 0; i < edges; ++i)
                 for (uint32_t n = 0; n < kWaitLimit && !bar_try(&sh.land[i & 3], (i >> 2) & 1); ++n) {
                 }
         }
         __syncwarp();
-    } else if (!Q4 && warp >= kSoftWarps + 2) {
+    } else if (!Q4 && warp == kSoftWarps + 3) {
         // ================================================ values no row, or not every row, sees
-        // the two warps take such tiles in turn
         const bool mixed = k.p_first != k.p_last;
         int edges = 0;
         for (int j = 0; j < nt; ++j) {
@@ -812,8 +811,6 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             if (attn_all_see(p, k, j0, kTile))
                 continue;
             const int e = edges++;
-            if ((e & 1) != warp - (kSoftWarps + 2))
-                continue;
             const int st = (2 * j + 1) % NST;
             if (!bar_wait(&sh.land[e & 3], (e >> 2) & 1, &sh.abort))
                 break;

@@ -6,11 +6,11 @@
 // words (c, w), for V the half words (2c, w) and (2c + 1, w).  One 16-byte (D =
 // 128) store a lane, every row in whole 32-byte sectors.
 //
-// s = e / -8 rounded up to 5 significant bits is bit arithmetic on fp32; the
-// quotient x / s and its rounding are IEEE, so equal inputs give equal codes on
-// any machine.
+// s = e / -8 rounded up to 5 significant bits is bit arithmetic on fp32, and the
+// codes are those of the exact quotient (code_of), so equal inputs give equal codes
+// on any machine.
 
-#include "cache_internal.cuh"
+#include "cache_attn.cuh"
 
 namespace qkr {
 namespace {
@@ -68,6 +68,18 @@ __device__ __forceinline__ float group_scale(float hi, float lo)
     return fminf(fmaxf(s, -31.f * 0x1p120f), 31.f * 0x1p120f);
 }
 
+// clamp(rint(x / s), -8, 7) + 8 from r = 1/s rounded.  x r is within 2^-21 of x / s;
+// adding 1536 rounds it to a multiple of 2^-13.  x has 8 significant bits and s 5,
+// so a quotient that is not half way between two codes is at least 2^-5 / 62 from
+// it, and one that is becomes exactly that: rint sees the true side and the true
+// ties (to even).  The last addition leaves the code in the low bits.
+__device__ __forceinline__ uint32_t code_of(float x, float r)
+{
+    float t = fmaf(x, r, 1536.f) - 1536.f;
+    t = fminf(fmaxf(t, -8.f), 7.f);
+    return __float_as_uint(t + 12582920.f) & 15u;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) set_rows_q4_kernel(const __grid_constant__ RowsQ4 p)
 {
@@ -91,33 +103,40 @@ __global__ void __launch_bounds__(kThreads) set_rows_q4_kernel(const __grid_cons
     uint32_t scale[GR / 2];  // bf16 pairs
 #pragma unroll
     for (int w = 0; w < GR; ++w) {
-        float f[8];
-        unpack8(v[w], f);
-        float hi = f[0], lo = f[0];
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            hi = fmaxf(hi, f[i]);
-            lo = fminf(lo, f[i]);
-            bad |= (__float_as_uint(f[i]) & 0x7f800000u) == 0x7f800000u;
-        }
-        uint32_t b = bad;
+        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v[w]);
+        const __nv_bfloat162 h2 = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        const __nv_bfloat162 l2 = __hmin2(__hmin2(h[0], h[1]), __hmin2(h[2], h[3]));
+        float hi = fmaxf(__low2float(h2), __high2float(h2));
+        float lo = fminf(__low2float(l2), __high2float(l2));
+        uint32_t top = __vmaxu2(__vmaxu2(v[w].x & 0x7fff7fffu, v[w].y & 0x7fff7fffu),
+                                __vmaxu2(v[w].z & 0x7fff7fffu, v[w].w & 0x7fff7fffu));
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
             hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
             lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            b |= __shfl_xor_sync(0xffffffffu, b, o);
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
         }
+        const bool bad = (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u;   // inf or NaN
         const float s = group_scale(hi, lo);
+        float f[8];
+        unpack8(v[w], f);
         uint32_t q = 0;
+        if (bad || s == 0.f) {
+            q = 0x88888888u;
+        } else if (fabsf(s) >= 0x1p-60f) {
+            const float r = __frcp_rn(s);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float c = s == 0.f || b ? 0.f : rintf(__fdiv_rn(f[i], s));
-            c = fminf(fmaxf(c, -8.f), 7.f);
-            q |= (uint32_t)((int)c + 8) << (4 * i);
+            for (int i = 0; i < 8; ++i)
+                q |= code_of(f[i], r) << (4 * i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float c = fminf(fmaxf(rintf(__fdiv_rn(f[i], s)), -8.f), 7.f);
+                q |= (uint32_t)((int)c + 8) << (4 * i);
+            }
         }
         code[w] = q;
-        const uint32_t bits = b ? 0x7fc0u : __float_as_uint(s) >> 16;
+        const uint32_t bits = bad ? 0x7fc0u : __float_as_uint(s) >> 16;
         if (w & 1)
             scale[w / 2] |= bits << 16;
         else
@@ -195,12 +214,20 @@ __global__ void __launch_bounds__(kThreads) get_rows_q4_kernel(const __grid_cons
     __nv_bfloat16 *dst = p.x[at.which] + at.t * p.ts[at.which] + at.head * D + 8 * at.lane4;
 #pragma unroll
     for (int w = 0; w < GR; ++w) {
-        const float s = __uint_as_float(w & 1 ? scale[w / 2] & 0xffff0000u : scale[w / 2] << 16);
-        float f[8];
+        // two elements a register, i and i + 4; every step is exact in bf16
+        const uint32_t s2 = w & 1 ? __byte_perm(scale[w / 2], 0, 0x3232)
+                                  : __byte_perm(scale[w / 2], 0, 0x1010);
+        uint32_t x[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            f[i] = (float)((int)(code[w] >> (4 * i) & 15u) - 8) * s;
-        st_stream(dst + 32 * w, pack8(f));
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t n = sub136(nibbles(code[w], i));
+            const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&n),
+                                             *reinterpret_cast<const __nv_bfloat162 *>(&s2));
+            x[i] = *reinterpret_cast<const uint32_t *>(&y);
+        }
+        st_stream(dst + 32 * w,
+                  make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410),
+                             __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632)));
     }
 }
 
