@@ -396,7 +396,7 @@ enum {
 
 /* A paged cache of K and V rows.  Row r of page p, head h starts at
  * base + p*page_stride + r*row_stride + h*head_stride, all strides in bytes
- * (any order of the axes, page and row strides below 2^32; rows of different (p, r, h) must not overlap).
+ * (any order of the axes, page and row strides below 2^32, head strides below 2^39; rows of different (p, r, h) must not overlap).
  * k, v hold the rows (QKR_CACHE_BF16: D bf16; QKR_CACHE_Q4: D/2 code bytes);
  * k_scale, v_scale the scales of QKR_CACHE_Q4 (NULL and ignored otherwise).
  * The flat row index of rope_set_rows and cache_set_rows_q4 is p*page_size + r.
@@ -447,7 +447,8 @@ typedef struct qkr_cache_desc {
  *                    tokens i*page_size ... of sequence b.
  *   lens             int32 device [B];  cu_q int32 device [B + 1], nondecreasing.
  *   max_q, max_len   host bounds of the new tokens of a sequence and of lens[b];
- *                    max_len <= table_stride * page_size.  They set the launch
+ *                    max_len <= table_stride * page_size.  B <= 2^16,
+ *                    T * Hq < 2^31, max_len <= 2^29.  They set the launch
  *                    shape only, so a captured graph serves any lengths up to them.
  *   scale            finite.   window, n_sink >= 0.
  *   workspace        device scratch of cache_attention_workspace() bytes, 16-byte

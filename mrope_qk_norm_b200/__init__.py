@@ -496,7 +496,6 @@ def _cache_common(fmt, k, D, tensors) -> CacheDesc:
     d.n_pages, d.page_size, d.Hkv, d.D = k.shape[0], k.shape[1], k.shape[2], D
     d._keep = tensors  # the descriptor holds raw pointers into these
     d._device, d._page, d._H, d._D = k.device, k.shape[1], k.shape[2], D
-    d._ref = ctypes.byref(d)
     return d
 
 
@@ -559,7 +558,7 @@ def cache_attention_workspace(q, cache: CacheDesc, batch, max_q, max_len, window
     """Bytes of workspace cache_attention needs for q [T, Hq, D] and these sizes."""
     n = ctypes.c_int64(0)
     T, Hq, _ = q.shape
-    _launch(cache._device, None, lambda s, *a: _lib.cache_attention_workspace(*a), cache._ref, T,
+    _launch(cache._device, None, lambda s, *a: _lib.cache_attention_workspace(*a), ctypes.byref(cache), T,
             Hq, batch, max_q, max_len, window, n_sink, ctypes.byref(n))
     return int(n.value)
 
@@ -612,7 +611,7 @@ def cache_attention(q, cache: CacheDesc, out, page_table, lens, cu_q, max_q, max
             raise ValueError("workspace must be contiguous")
         ws_n = workspace.nbytes
         ws_p = _arg(workspace, workspace.dtype, dev, "workspace")
-    _launch(dev, stream, _lib.cache_attention, cache._ref, _arg(q, bf, dev, "q"),
+    _launch(dev, stream, _lib.cache_attention, ctypes.byref(cache), _arg(q, bf, dev, "q"),
             _arg(out, bf, dev, "out"), lse_p, T, Hq, qt, qh if Hq > 1 else D,
             ot if T > 1 else Hq * D, _arg(page_table, i32, dev, "page_table"), tb,
             _arg(lens, i32, dev, "lens"), _arg(cu_q, i32, dev, "cu_q"), B, max_q, max_len,
@@ -634,7 +633,7 @@ def _rows_q4(fn, k, v, cache, row_idx, stream):
     if T <= 1:
         kt = vt = H * D
     bf = torch.bfloat16
-    _launch(dev, stream, fn, cache._ref, _arg(k, bf, dev, "k"), _arg(v, bf, dev, "v"),
+    _launch(dev, stream, fn, ctypes.byref(cache), _arg(k, bf, dev, "k"), _arg(v, bf, dev, "v"),
             _arg(row_idx, torch.int64, dev, "row_idx"), T, kt, vt)
 
 

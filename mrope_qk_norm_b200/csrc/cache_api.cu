@@ -4,9 +4,6 @@
 #include <cfloat>
 #include <climits>
 #include <cmath>
-#include <mutex>
-#include <set>
-#include <utility>
 
 #include "cache_internal.cuh"
 
@@ -58,11 +55,9 @@ qkr_status check_plane(const char *name, const qkr_cache_plane &in, const qkr_ca
         if (use[i] % align)
             return api_fail(QKR_ERR_UNSUPPORTED, "cache %s: strides must be multiples of %lld bytes",
                             name, (long long)align);
-        if (i < 2 && use[i] >= (int64_t)1 << 32)
+        if (use[i] >= (int64_t)1 << (i < 2 ? 32 : 39))
             return api_fail(QKR_ERR_UNSUPPORTED, "cache %s: page and row strides must be below 2^32 "
-                            "bytes", name);
-        if (use[i] > ((int64_t)1 << 50) / extent[i])
-            return api_fail(QKR_ERR_INVALID_ARG, "cache %s exceeds the address range", name);
+                            "bytes, head strides below 2^39", name);
     }
     out->base = static_cast<uint8_t *>(in.base);
     out->ps = use[0];
@@ -154,8 +149,14 @@ struct Device {
 };
 Device g_devices[kMaxDevices];
 
-std::mutex g_smem_mu;
-std::set<std::pair<int, const void *>> g_smem;   // kernels allowed, by device
+// Kernels allowed their dynamic shared memory, a bit a device.  Nothing here
+// allocates or throws; two threads that ask at once both ask the driver.
+constexpr int kMaxKernels = 64;
+struct SmemSeen {
+    std::atomic<const void *> fn{nullptr};
+    std::atomic<uint64_t> devices{0};
+};
+SmemSeen g_smem[kMaxKernels];
 
 qkr_status current_device(int *sms, unsigned **status)
 {
@@ -196,8 +197,8 @@ qkr_status check_sizes(Sizes &s)
     if (s.Hq < 1 || s.Hq % s.Hkv || s.Hq > 65536)
         return api_fail(QKR_ERR_INVALID_ARG, "Hq (%lld) must be a multiple of Hkv (%lld), at most "
                         "65536", (long long)s.Hq, (long long)s.Hkv);
-    if (s.T > INT_MAX || s.T * s.Hq > INT_MAX || s.B > (1 << 24) || s.max_len > (1 << 30))
-        return api_fail(QKR_ERR_UNSUPPORTED, "T * Hq < 2^31, B <= 2^24, max_len <= 2^30");
+    if (s.T > INT_MAX || s.T * s.Hq > INT_MAX || s.B > (1 << 16) || s.max_len > (1 << 29))
+        return api_fail(QKR_ERR_UNSUPPORTED, "need T * Hq < 2^31, B <= 2^16, max_len <= 2^29");
     if (s.window < 0 || s.n_sink < 0)
         return api_fail(QKR_ERR_INVALID_ARG, "window and n_sink must be >= 0");
     if (s.max_q > s.T)
@@ -320,12 +321,20 @@ cudaError_t qkr::allow_smem(const void *fn, int bytes)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
-    std::lock_guard<std::mutex> lock(g_smem_mu);
-    if (g_smem.count({dev, fn}))
+    SmemSeen *seen = nullptr;
+    for (SmemSeen &k : g_smem) {
+        const void *have = nullptr;
+        if (k.fn.compare_exchange_strong(have, fn) || have == fn) {
+            seen = &k;
+            break;
+        }
+    }
+    const uint64_t bit = dev >= 0 && dev < kMaxDevices ? (uint64_t)1 << dev : 0;
+    if (seen && (seen->devices.load() & bit))
         return cudaSuccess;
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess)
-        g_smem.insert({dev, fn});
+    if (e == cudaSuccess && seen)
+        seen->devices.fetch_or(bit);
     return e;
 }
 

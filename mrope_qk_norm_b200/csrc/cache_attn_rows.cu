@@ -1041,7 +1041,9 @@ attn_rows_join_kernel(const __grid_constant__ AttnParams p, int used)
     __shared__ float sm_o[kWarps][DP];
     __shared__ float sm_l[kWarps], sm_m[kWarps];
     pdl_wait();
-    pdl_trigger();
+    // no early launch of the next kernel: were it another even-shares one, its CTAs
+    // would find the SMs unevenly full and some come a wave late (decode_window, back
+    // to back: 39 us against 33)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cta = (int)(blockIdx.x / (uint32_t)used), r = (int)(blockIdx.x % (uint32_t)used);
     const AttnSpan s = p.ws_span[cta];

@@ -65,7 +65,7 @@ def test_a_valid_call_passes_validation():
     (E, dict(max_len=129)), (E, dict(tstride=-1)),
     (U, dict(q=BASE + 8)), (U, dict(out=BASE + (5 << 30) + 8)), (U, dict(lens=BASE + (7 << 30) + 2)),
     (U, dict(qts=252)), (U, dict(qhs=32)), (U, dict(qts=-256)), (U, dict(ots=128)), (U, dict(ots=260)),
-    (U, dict(T=1 << 30)), (U, dict(max_len=1 << 31, tstride=1 << 30)),
+    (U, dict(T=1 << 30)), (U, dict(max_len=(1 << 29) + 1, tstride=1 << 30)), (U, dict(B=(1 << 16) + 1)),
 ])
 def test_attention_refusals(status, kw):
     assert _attend(**kw) == status, _message()
@@ -78,7 +78,7 @@ def test_attention_refusals(status, kw):
     (U, dict(fmt=qkr.CACHE_Q4, D=96)), (U, dict(fmt=qkr.CACHE_Q4, D=32)),
     (E, dict(k__base=0)), (U, dict(v__base=BASE + 8)), (U, dict(k__row_stride=250)),
     (U, dict(k__row_stride=264)), (U, dict(v__head_stride=0)), (U, dict(k__page_stride=-4096)),
-    (U, dict(k__page_stride=1 << 32)), (U, dict(v__row_stride=1 << 32)), (E, dict(k__head_stride=1 << 50)),
+    (U, dict(k__page_stride=1 << 32)), (U, dict(v__row_stride=1 << 32)), (U, dict(k__head_stride=1 << 39)),
     (E, dict(fmt=qkr.CACHE_Q4, k_scale__base=0)), (U, dict(fmt=qkr.CACHE_Q4, v_scale__base=BASE + 2)),
 ])
 def test_cache_refusals(status, kw):
@@ -124,3 +124,19 @@ def test_workspace_refusals():
     assert need(out=None) == E and need(Hq=5) == E and need(T=-1) == E and need(w=-1) == E
     assert need(cache=_cache(fmt=7)) == E
     assert need(T=0) == qkr.QKR_OK and n.value == 0
+
+
+def test_the_descriptor_is_no_cycle():
+    """Dropping a descriptor frees the cache tensors at once, without the collector."""
+    import gc
+    import weakref
+    d = _cache()
+    d._keep = keep = type("T", (), {})()
+    r = weakref.ref(keep)
+    gc.disable()
+    try:
+        _attend(d)
+        del d, keep
+        assert r() is None
+    finally:
+        gc.enable()

@@ -216,6 +216,76 @@ def test_bad_metadata_is_clamped_and_reported(fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("layout", ["padded", "one_tensor", "heads_outermost"])
+def test_strides(fmt, layout):
+    """Rows, heads and pages padded by odd multiples of the alignment; K and V in
+    one tensor; a plane a head."""
+    b = Batch(n=[1, 70, 3], lens=[200, 150, 90], hq=6, hkv=3, D=64, page=16, fmt=fmt, seed=17,
+              window=100, sink=3)
+    planes = []
+    for x in b.planes:
+        P, ps, H, w = x.shape
+        unit = 16 // x.element_size() if w * x.element_size() >= 16 else w
+        if layout == "padded":
+            hs, rs = w + unit, (w + unit) * H + 3 * unit
+            pg = rs * ps + 5 * unit
+        elif layout == "one_tensor":
+            hs, rs, pg = w, w * H, 2 * w * H * ps
+        else:
+            rs, pg = w, w * ps
+            hs = pg * P + 7 * unit
+        size = (P - 1) * pg + (ps - 1) * rs + (H - 1) * hs + w
+        buf = torch.empty(size + 64, dtype=x.dtype, device="cuda")
+        buf.view(torch.uint8).fill_(0xff)
+        y = buf.as_strided(x.shape, (pg, rs, hs, 1))
+        y.copy_(x)
+        planes.append(y)
+    if layout == "one_tensor":
+        k, v = (planes[0], planes[1]) if fmt == "bf16" else (planes[0], planes[2])
+        P, ps, H, w = k.shape
+        both = torch.empty((P, 2, ps, H, w), dtype=k.dtype, device="cuda")
+        both[:, 0], both[:, 1] = k, v
+        planes[0], planes[1 if fmt == "bf16" else 2] = both[:, 0], both[:, 1]
+    b.planes = planes
+    b.cache = (qkr.cache_desc if fmt == "bf16" else qkr.cache_desc_q4)(*planes)
+    b.call()
+    torch.cuda.synchronize()
+    b.check()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_nonfinite_query_stays_in_its_row(fmt):
+    for n in (3, 90):
+        b = Batch(n=[n], lens=[n + 40], hq=4, hkv=2, D=64, page=16, fmt=fmt, seed=18, poison=False)
+        ref = Batch(n=[n], lens=[n + 40], hq=4, hkv=2, D=64, page=16, fmt=fmt, seed=18,
+                    poison=False)
+        b.q[1, 2, 7] = float("nan")
+        b.call()
+        ref.call()
+        torch.cuda.synchronize()
+        assert torch.isnan(b.out[1, 2]).all()
+        b.out[1, 2] = ref.out[1, 2]
+        assert torch.equal(b.out[:n].view(torch.int16), ref.out[:n].view(torch.int16))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n", [1, 40])
+def test_huge_values_behind_the_mask(fmt, n):
+    """The largest finite numbers in keys a token does not see leave no trace."""
+    b = Batch(n=[n], lens=[n + 300], hq=2, hkv=2, D=64, page=16, fmt=fmt, seed=19, poison=False,
+              window=40, sink=2)
+    plain = Batch(n=[n], lens=[n + 300], hq=2, hkv=2, D=64, page=16, fmt=fmt, seed=19,
+                  poison=False, window=40, sink=2)
+    for pl in b.planes:
+        if pl.dtype == torch.bfloat16:
+            pl[~b.seen] = 3.3e38     # rows that no token sees
+    b.call()
+    plain.call()
+    torch.cuda.synchronize()
+    assert torch.equal(b.out[:n].view(torch.int16), plain.out[:n].view(torch.int16))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_far_rows(fmt):
     """Pages whose rows lie beyond 2^31 bytes (and elements, for bf16)."""
     D, hkv, page = 64, 1, 16
