@@ -548,7 +548,7 @@ def _launch(device, stream, fn, *args):
 def _arg(t, dtype, device, what) -> int:
     if t.dtype is not dtype:
         raise ValueError("%s must be %s, got %s" % (what, dtype, t.dtype))
-    if t.device != device:
+    if t.get_device() != device.index:
         raise ValueError("%s must be on the cache's device %s" % (what, device))
     return t.data_ptr()
 

@@ -281,8 +281,9 @@ qkr_status make_plan(const Sizes &s, int64_t page_size, Plan *plan)
         const int64_t slots = (int64_t)sms * qkr::attn_rows_resident(s.D, p.rows, s.q4);
         // A cluster a block, as large as leaves a warp 32 keys and the clusters
         // room, where a warp then has at most 96 keys.  Else even shares, of no
-        // less than 128 keys; a block counts for 128 keys more (8192-key decode
-        // batch: 88 us at 0, 72 at 128).
+        // less than 128 keys; a block counts for 128 keys more, 512 in 4 bits, whose
+        // keys take less time (ragged decode batches, bf16: 88 us at 0, 72 at 128, 74
+        // at 512; 4 bits: 60 at 128, 53 at 512).
         p.nsplit = 1;
         int64_t size = 1;
         while (size < 8 && keys > size * 128 && items * size * 2 <= slots)
@@ -292,7 +293,7 @@ qkr_status make_plan(const Sizes &s, int64_t page_size, Plan *plan)
         } else {
             p.ctas = (int)slots;
             p.split_tiles = 128 >> shift;
-            p.piece_cost = 128 >> shift;
+            p.piece_cost = (s.q4 ? 512 : 128) >> shift;
             plan->ws_bytes = slots * (2 * p.rows * (s.D + 2) * 4 + (int64_t)sizeof(qkr::AttnSpan));
         }
     }

@@ -961,14 +961,26 @@ attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
     const bool feeds = warp == kWarps;
     RingAt<R::kStages> it;
     bool first = true;
+    // cu and lens of the next sequence are asked for while this one is worked on
+    int cu0 = p.cu[b], cu1 = p.cu[b + 1], len = p.lens[b];
     while (at < end) {
         // the next sequence with rows of this launch
         int64_t t0;
         bool bad;
-        int n = attn_seq(p, b, &t0, &bad);
-        while (!attn_blocks_of(p, n))
-            n = attn_seq(p, ++b, &t0, &bad);
-        const AttnBlock k = attn_block_at(p, b, 0, n, t0, bad);
+        int n = attn_clamp(p, cu0, cu1, &t0, &bad);
+        while (!attn_blocks_of(p, n)) {
+            ++b;
+            cu0 = cu1;
+            cu1 = p.cu[b + 1];
+            len = p.lens[b];
+            n = attn_clamp(p, cu0, cu1, &t0, &bad);
+        }
+        const AttnBlock k = attn_block_of(p, b, 0, n, len, t0, bad);
+        cu0 = cu1;
+        if (b + 1 < p.B) {
+            cu1 = p.cu[b + 2];
+            len = p.lens[b + 1];
+        }
         const int tiles = max(1, k.ntiles), cost = p.piece_cost + tiles;
         const int64_t off = at - before * Hkv;
         int kvh = (int)(off / cost), from = (int)(off % cost);

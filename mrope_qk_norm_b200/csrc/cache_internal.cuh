@@ -84,16 +84,21 @@ struct AttnBlock {
     __device__ __forceinline__ int tile_at(int i) const { return i < c_sink ? i : c0 + i - c_sink; }
 };
 
-// New tokens and start of sequence b, clamped into [0, T] and max_q.
-__device__ __forceinline__ int attn_seq(const AttnParams &p, int b, int64_t *t0, bool *bad)
+// New tokens and start of the sequence between cu entries a and e, clamped into
+// [0, T] and max_q.
+__device__ __forceinline__ int attn_clamp(const AttnParams &p, int64_t a, int64_t e, int64_t *t0,
+                                          bool *bad)
 {
-    const int64_t a = p.cu[b], e = p.cu[b + 1];
     const int64_t s = a < 0 ? 0 : (a > p.T ? p.T : a);
     int64_t n = (e > p.T ? p.T : e) - s;
     n = n < 0 ? 0 : (n > p.max_q ? p.max_q : n);
     *bad = a < 0 || e > p.T || e < a || e - a > p.max_q;
     *t0 = s;
     return (int)n;
+}
+__device__ __forceinline__ int attn_seq(const AttnParams &p, int b, int64_t *t0, bool *bad)
+{
+    return attn_clamp(p, p.cu[b], p.cu[b + 1], t0, bad);
 }
 
 __device__ __forceinline__ int attn_blocks_of(const AttnParams &p, int n)
@@ -102,12 +107,11 @@ __device__ __forceinline__ int attn_blocks_of(const AttnParams &p, int n)
     return r > p.rows_lo && r <= p.rows_hi ? (int)((r + p.rows - 1) / p.rows) : 0;
 }
 
-// Block `blk` of sequence b (n new tokens from t0 on) and what it sees.
-__device__ __forceinline__ AttnBlock attn_block_at(const AttnParams &p, int b, int blk, int n,
+// Block `blk` of sequence b (n new tokens from t0 on, lens entry L) and what it sees.
+__device__ __forceinline__ AttnBlock attn_block_of(const AttnParams &p, int b, int blk, int n, int L,
                                                    int64_t t0, bool bad)
 {
     AttnBlock k;
-    int L = p.lens[b];
     if (L < 0 || L > p.max_len) {
         bad = true;
         L = L < 0 ? 0 : p.max_len;
@@ -131,6 +135,12 @@ __device__ __forceinline__ AttnBlock attn_block_at(const AttnParams &p, int b, i
     const int c1 = (k.hi + p.tile - 1) / p.tile;
     k.ntiles = k.c_sink + max(0, c1 - k.c0);
     return k;
+}
+
+__device__ __forceinline__ AttnBlock attn_block_at(const AttnParams &p, int b, int blk, int n,
+                                                   int64_t t0, bool bad)
+{
+    return attn_block_of(p, b, blk, n, p.lens[b], t0, bad);
 }
 
 // The block of block index `idx`, computed by a whole warp.  Where the blocks
