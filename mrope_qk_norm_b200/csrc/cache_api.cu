@@ -301,12 +301,28 @@ qkr_status make_plan(const Sizes &s, int64_t page_size, Plan *plan)
         qkr::AttnParams &p = plan->pt;
         p.tile_shift = 7;
         const int64_t tiles = blocks(s, 256, 128, plan->rows ? kFewRows : 0, INT_MAX, &p);
-        // A block's keys are cut only where the blocks alone do not fill the
-        // SMs: a part costs 256 partial rows written and read again.
-        const int64_t items = p.n_blocks * s.Hkv;
-        const int64_t want = items >= sms ? 1 : (2 * sms + items - 1) / items;
-        int64_t split = (tiles + want - 1) / want;
-        cut(s, tiles, split < 4 ? 4 : split, &p, &plan->ws_bytes);
+        // Parts of a block's keys: the number that takes the fewest rounds over the
+        // SMs times what a CTA then does, its tiles and some 5 tiles' time of setting
+        // up and writing out (20 of 3400 clocks a tile); joining parts costs 3 more.
+        // A sequence's last block is counted half (q4_prefill_chunk: 142 us in 3
+        // parts, 106 whole).
+        const int64_t most_items = p.n_blocks * s.Hkv;
+        int64_t items = (s.T * G / 256 + (s.B + 1) / 2) * s.Hkv;
+        if (items > most_items)
+            items = most_items;
+        if (items < 1)
+            items = 1;
+        int64_t best = 1, best_cost = INT64_MAX;
+        // (with two rounds or more the blocks' own lengths even out)
+        for (int64_t n = 1; n <= (items >= 2 * sms ? 1 : 64) && n <= tiles; ++n) {
+            const int64_t rounds = (items * n + sms - 1) / sms;
+            const int64_t cost = rounds * ((tiles + n - 1) / n + 5) + (n > 1 ? 3 : 0);
+            if (cost < best_cost) {
+                best_cost = cost;
+                best = n;
+            }
+        }
+        cut(s, tiles, (tiles + best - 1) / best, &p, &plan->ws_bytes);
     }
     if ((plan->rows && plan->pr.n_blocks * s.Hkv > INT_MAX / 256) ||
         (plan->tiles && plan->pt.n_blocks * s.Hkv * plan->pt.nsplit > INT_MAX / 256))

@@ -63,10 +63,9 @@ namespace {
 
 constexpr int kWarps = 4;              // computing warps; one more feeds them
 constexpr int kThreads = 32 * (kWarps + 1);
-// A wait asks the hardware to sleep up to kWaitHint ns, kWaitLimit times at most.
-// (Without the hint it returns after some 50 clocks: the polls were a quarter of
-// all instructions.)
-constexpr uint32_t kWaitHint = 100000, kWaitLimit = 1u << 14;
+// A wait asks so often at most.  Roles that run ahead sleep in between (their polls
+// would take issue slots from the others).
+constexpr uint32_t kWaitLimit = 1u << 21;
 constexpr uint32_t kMinus136 = 0xc308c308u;  // bf16 pair
 constexpr float kSlack = 8.f;  // log2 units the reference may lag behind the maximum
 
@@ -174,27 +173,29 @@ __device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity)
     uint32_t ok;
     asm volatile(
         "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
         " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok) : "r"(sm_u32(bar)), "r"(parity), "r"(kWaitHint) : "memory");
+        : "=r"(ok) : "r"(sm_u32(bar)), "r"(parity) : "memory");
     return ok != 0;
 }
 // Bounded; after a wait that ran out no other waits (the result is reported as
 // not valid, nothing is accessed that would not be otherwise).
-__device__ __noinline__ void bar_wait_long(uint64_t *bar, uint32_t parity, int *abort)
+__device__ __noinline__ void bar_wait_long(uint64_t *bar, uint32_t parity, int *abort, int sleep)
 {
     for (uint32_t i = 0; i < kWaitLimit; ++i) {
         if (bar_try(bar, parity))
             return;
         if (*reinterpret_cast<volatile int *>(abort))
             return;
+        if (sleep)
+            __nanosleep(sleep);
     }
     *reinterpret_cast<volatile int *>(abort) = 1;
 }
-__device__ __forceinline__ void bar_wait(uint64_t *bar, uint32_t parity, int *abort)
+__device__ __forceinline__ void bar_wait(uint64_t *bar, uint32_t parity, int *abort, int sleep = 0)
 {
     if (!__all_sync(0xffffffffu, bar_try(bar, parity)))
-        bar_wait_long(bar, parity, abort);
+        bar_wait_long(bar, parity, abort, sleep);
 }
 
 // A warp's place in the ring.
@@ -290,7 +291,7 @@ __device__ __forceinline__ void attn_feed(const AttnParams &p, const CacheMaps &
             page = -1;
         }
         // (the stages' first use finds the phase before the first complete)
-        bar_wait(&sh.empty[st], at->phase ^ 1u, &sh.abort);
+        bar_wait(&sh.empty[st], at->phase ^ 1u, &sh.abort, 100);
         __syncwarp();
         const bool by_bulk = !scales || p.dense_scales;
         const bool copies = page >= 0 || (page == -1 && !scales);

@@ -61,10 +61,10 @@ constexpr int kPolyEvery = 8;
 constexpr float kExpC0 = 0.9999992847442627f, kExpC1 = 0.6931217908859253f,
                 kExpC2 = 0.240247443318367f, kExpC3 = 0.05591785907745361f,
                 kExpC4 = 0.009570100344717503f;
-// A wait asks the hardware to sleep up to kWaitHint ns, kWaitLimit times at most.
-// (Without the hint it returns after some 50 clocks: the polls were a quarter of
-// all instructions.)
-constexpr uint32_t kWaitHint = 100000, kWaitLimit = 1u << 14;
+// A wait asks so often at most.  Roles that run ahead sleep in between (their polls
+// would take issue slots from the others).
+constexpr uint32_t kWaitLimit = 1u << 21;
+constexpr int kAhead = 200;              // ns
 
 struct Shared {
     uint64_t raw[8], empty[8];            // ring: full, free
@@ -109,12 +109,13 @@ __device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity)
     uint32_t ok;
     asm volatile(
         "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
         " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok) : "r"(smem_u32(b)), "r"(parity), "r"(kWaitHint) : "memory");
+        : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
     return ok != 0;
 }
 // By a whole warp.  False when the wait ran out or another role's has.
+template <int SLEEP>
 __device__ __forceinline__ bool bar_wait_long(uint64_t *b, uint32_t parity, int *abort)
 {
     for (uint32_t i = 0; i < kWaitLimit; ++i) {
@@ -122,15 +123,18 @@ __device__ __forceinline__ bool bar_wait_long(uint64_t *b, uint32_t parity, int 
             return true;
         if (*reinterpret_cast<volatile int *>(abort))
             return false;
+        if constexpr (SLEEP > 0)
+            __nanosleep(SLEEP);
     }
     *reinterpret_cast<volatile int *>(abort) = 1;
     return false;
 }
+template <int SLEEP = 0>
 __device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, int *abort)
 {
     if (__all_sync(0xffffffffu, bar_try(b, parity)))
         return true;
-    return __all_sync(0xffffffffu, bar_wait_long(b, parity, abort));
+    return __all_sync(0xffffffffu, bar_wait_long<SLEEP>(b, parity, abort));
 }
 
 __device__ __forceinline__ void fence_async()
@@ -764,7 +768,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             const int it = 2 * j + is_v, st = it % NST;
             look(j + 1, &page_next, &row_next);
             if (it >= NST)
-                ok = bar_wait(&sh.empty[st], (it / NST - 1) & 1, &sh.abort);
+                ok = bar_wait<kAhead>(&sh.empty[st], (it / NST - 1) & 1, &sh.abort);
             if (!ok)
                 break;
             // the values of a tile that not every row sees go past a clearing warp
@@ -812,7 +816,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                 continue;
             const int e = edges++;
             const int st = (2 * j + 1) % NST;
-            if (!bar_wait(&sh.land[e & 3], (e >> 2) & 1, &sh.abort))
+            if (!bar_wait<kAhead>(&sh.land[e & 3], (e >> 2) & 1, &sh.abort))
                 break;
             uint8_t *tile = ring + st * Lay::kStageBytes;
             // keys no row sees: [z0, z1) and [z2, 128)
@@ -898,7 +902,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             const int st = it % NST;
             const bool is_v = it & 1;
             if (it >= NST) {
-                ok = bar_wait(&sh.empty[st], (it / NST - 1) & 1, &sh.abort);
+                ok = bar_wait<kAhead>(&sh.empty[st], (it / NST - 1) & 1, &sh.abort);
                 if (!ok)
                     break;
             }
