@@ -461,8 +461,9 @@ typedef struct qkr_cache_desc {
  * bit 8 of the device status word.
  * The maximum, the sum and the output are held in fp32; the weights exp(s - m)
  * are rounded to bf16 for their product with V, and out once at the end.
- * Enqueues one kernel, or two: a second where sequences of a few rows and of
- * many can stand side by side, or where one joins the parts of a long axis.
+ * Enqueues one kernel for sequences of few rows (new tokens times query heads of a
+ * KV head, up to 16) or of many, or one for each where both can stand side by
+ * side, and after either one that joins the parts of a split axis.
  */
 qkr_status cache_attention(void *stream, const qkr_cache_desc *cache, const void *q, void *out,
                            float *lse, int64_t T, int64_t Hq, int64_t q_tok_stride,

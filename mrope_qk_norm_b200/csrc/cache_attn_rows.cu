@@ -22,9 +22,12 @@
 // below makes the operand loads of eight lanes meet eight different banks in
 // the layout the copies leave.  Where a scale row is not one of a dense run,
 // its 8 (4) bytes come by cp.async.  Before this the warps loaded their own
-// operands into registers (q4_decode_long 141 us: three warps a scheduler, each
-// waiting for its own loads), and with a feeding warp that copied 16 bytes a
-// lane that warp was the bound (decode_long 344 us against 146).
+// operands into registers (two sequences of 130,000 tokens in 4 bits, 8 KV heads of
+// 128: 141 us, three warps a scheduler each waiting for its own loads; now 95), and
+// with a feeding warp that copied 16 bytes a lane that warp was the bound (100,000
+// tokens in bf16: 344 us against 146; now 134, 95% of the copy rate).  4 bits is
+// bound by instructions: about 400 a 16 keys, half of them on the half-rate integer
+// pipe, which nibbles keep busy for as long as HBM needs for the bytes.
 //
 // Who takes which keys.  Much work: as many CTAs as stay resident, each with the
 // same number of tiles of the row (sequence, KV head, tile), found on the device
@@ -1055,8 +1058,8 @@ attn_rows_join_kernel(const __grid_constant__ AttnParams p, int used)
     __shared__ float sm_l[kWarps], sm_m[kWarps];
     pdl_wait();
     // no early launch of the next kernel: were it another even-shares one, its CTAs
-    // would find the SMs unevenly full and some come a wave late (decode_window, back
-    // to back: 39 us against 33)
+    // would find the SMs unevenly full and some come a wave late (64 sequences,
+    // window 1000, back to back: 39 us against 32)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cta = (int)(blockIdx.x / (uint32_t)used), r = (int)(blockIdx.x % (uint32_t)used);
     const AttnSpan s = p.ws_span[cta];

@@ -9,9 +9,8 @@
 // memory.  Tensor memory: S0 | S1 | O0 | O1.
 //
 // Two threads share a row, 64 scores each, because the softmax's latency is what
-// the tensor cores wait for (one thread a row: 3470 clocks per 128 keys of a
-// block, 2048 of which the tensor cores work); the two agree on the reference
-// through a named barrier.  The softmax warps take registers from the others
+// the tensor cores wait for; the two agree on the reference through a named
+// barrier.  The softmax warps take registers from the others
 // (setmaxnreg): 4 x 104 + 64 of the 5 x 96 launched (4 bits: 4 x 88 + 2 x 64 of
 // 6 x 80).
 //
@@ -27,7 +26,12 @@
 // Per tile and 128 keys at D = 128 the two products take 1024 clocks of the
 // tensor cores and the 16384 exponentials 1024 clocks of the SM's exponential
 // units, so these two bound the kernel together; loads are 64 KB per 2048
-// clocks and mostly hit L2.
+// clocks and mostly hit L2.  Measured: 3300 to 3400 clocks per 128 keys of a block
+// instead of 2048 (a tile's softmax, 1700 to 2100 clocks, and its two products follow
+// one another, and two tiles hide only part of that), and some 18,000 clocks a block
+// for setting up and writing out.  A prompt of 8192 tokens, 16 heads over 8 of 128:
+// 289 us, 0.95 PFLOP/s (250 us and 1.1 where launches stand apart and the clock is
+// higher).
 //
 // The running maximum is a reference that moves only when a score exceeds it by
 // 2^8: the usual tile leaves O alone, and a weight stays below 2^8.  When the
@@ -57,6 +61,8 @@ constexpr int kSoftWarps = 16;
 constexpr int tiles_threads(bool q4) { return 32 * (kSoftWarps + (q4 ? 8 : 4)); }
 constexpr int kTile = 128;               // keys of a tile, rows of a tile
 constexpr float kSlack = 8.f;
+// One pair of exponentials in 8 on the FMA pipe (8192-token prompt: 251 us; every
+// fourth 257, none 257).
 constexpr int kPolyEvery = 8;
 constexpr float kExpC0 = 0.9999992847442627f, kExpC1 = 0.6931217908859253f,
                 kExpC2 = 0.240247443318367f, kExpC3 = 0.05591785907745361f,

@@ -3,11 +3,17 @@ import ctypes
 
 import pytest
 import torch
+from hypothesis import HealthCheck, given, settings
+from hypothesis import strategies as st
 
 import mrope_qk_norm_b200 as qkr
 
 BASE = 1 << 36
 E, U = 1, 2
+ptrs = st.one_of(st.just(0), st.integers(0, 1 << 24).map(lambda o: BASE + o))
+small = st.integers(-3, 300)
+wide = st.one_of(small, st.integers(-(1 << 33), 1 << 33))
+big = st.one_of(st.integers(0, 64).map(lambda x: 64 * x), st.integers(-(1 << 40), 1 << 40))
 
 pytestmark = pytest.mark.skipif(torch.cuda.is_available(),
                                 reason="an accepted call would launch on the fake addresses")
@@ -113,6 +119,30 @@ def test_empty_calls_enqueue_nothing():
     for kw in (dict(T=0), dict(B=0), dict(max_q=0)):
         assert _attend(**kw, q=0, out=0, lens=0, cu=0, table=0, ws=0) == qkr.QKR_OK
         assert qkr.last_launch()["launches"] == 0
+
+
+@settings(max_examples=500, deadline=None, suppress_health_check=list(HealthCheck))
+@given(fmt=st.integers(-1, 2), page=st.integers(-16, 1 << 17), pages=st.integers(-2, 1 << 33),
+       heads=st.integers(-1, 70), D=st.integers(-8, 300), bases=st.lists(ptrs, min_size=4, max_size=4),
+       strides=st.lists(big, min_size=12, max_size=12), args=st.lists(ptrs, min_size=7, max_size=7),
+       T=wide, Hq=small, ss=st.lists(big, min_size=4, max_size=4), B=wide, mq=wide, ml=wide,
+       scale=st.floats(allow_nan=True, allow_infinity=True), w=big, sink=big, wsb=big)
+def test_fuzz(fmt, page, pages, heads, D, bases, strides, args, T, Hq, ss, B, mq, ml, scale, w, sink,
+              wsb):
+    """Any sizes, strides and pointers come back as a status code with a message."""
+    c = qkr.CacheDesc(format=fmt, page_size=page, n_pages=pages, Hkv=heads, D=D)
+    c.k, c.v, c.k_scale, c.v_scale = (qkr.CachePlane(bases[i], *strides[3 * i:3 * i + 3])
+                                      for i in range(4))
+    L, n = qkr.lib(), ctypes.c_int64(0)
+    calls = [L.cache_attention(None, ctypes.byref(c), args[0], args[1], args[2], T, Hq, ss[0], ss[1],
+                               ss[2], args[3], ss[3], args[4], args[5], B, mq, ml, scale, w, sink,
+                               args[6], wsb),
+             L.cache_set_rows_q4(None, ctypes.byref(c), args[0], args[1], args[2], T, ss[0], ss[1]),
+             L.cache_get_rows_q4(None, ctypes.byref(c), args[0], args[1], args[2], T, ss[0], ss[1]),
+             L.cache_attention_workspace(ctypes.byref(c), T, Hq, B, mq, ml, w, sink,
+                                         ctypes.byref(n))]
+    for status in calls:
+        assert status in (qkr.QKR_OK, E, U, qkr.QKR_ERR_CUDA)
 
 
 def test_workspace_refusals():
