@@ -268,44 +268,45 @@ __device__ __forceinline__ void attn_feed(const AttnParams &p, const CacheMaps &
     const uint32_t to = 2 * R::kPart + ((is_v ? R::kKeys : 0) + first) * R::kScale;   // scales
     const uint32_t bytes = scales ? box * R::kScale : box * R::kRowPart;
     const int32_t *table = p.table + (int64_t)k.b * p.table_stride;
-    // this lane's run of keys in the stage at tile i: its page (-1: none; -2: no
-    // key of it is seen by any row) and the row there
-    auto look = [&](int i, int *page, int *row) {
-        *page = -2;
+    // this lane's tile of the stage at tile i: false past the piece's end, else its
+    // page as the table has it and the row there
+    auto look = [&](int i, int *page, int *row) -> bool {
+        *page = -1;
         *row = 0;
         i += first >> p.tile_shift;
         if (!mine || i >= i1)
-            return;
+            return false;
         const int at = k.tile_at(i);
         // division by the tiles of a page: exact for tiles below 2^26
         const int pg = (int)((uint64_t)at * p.page_recip >> 38);
         *row = (at << p.tile_shift) - pg * p.c.page_size;
         *page = table[pg];
+        return true;
     };
     int page, row;
-    look(i0, &page, &row);
+    bool wanted = look(i0, &page, &row);
     for (int i = i0; i < i1; i += step, at->next()) {
         const int st = at->st;
         const uint32_t bar = sm_u32(&sh.full[st]);
         int page_next, row_next;
-        look(i + step, &page_next, &row_next);
-        if (page != -2 && (unsigned)page >= (unsigned)p.c.n_pages) {
+        const bool wanted_next = look(i + step, &page_next, &row_next);
+        if (wanted && (unsigned)page >= (unsigned)p.c.n_pages) {
             atomicOr(p.status, kStatusBounds);
-            page = -1;
+            page = -1;      // reads as zeros
         }
         // (the stages' first use finds the phase before the first complete)
         bar_wait(&sh.empty[st], at->phase ^ 1u, &sh.abort, 100);
         __syncwarp();
         const bool by_bulk = !scales || p.dense_scales;
-        const bool copies = page >= 0 || (page == -1 && !scales);
-        const bool issue = by_bulk && copies;
-        if (scales && p.dense_scales && page == -1)      // scales of a page that does not exist
+        const bool issue = by_bulk && wanted && (page >= 0 || !scales);
+        if (wanted && scales && p.dense_scales && page < 0)
             for (int x = 0; x < (int)bytes; x += 16)
                 *reinterpret_cast<uint4 *>(ring + st * R::kStageBytes + to + x) = make_uint4(0, 0, 0, 0);
         uint32_t total = issue ? bytes : 0;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             total += __shfl_xor_sync(0xffffffffu, total, o);
+        __syncwarp();       // the zeros above come before the arrival
         if (lane == 0)
             bar_expect(&sh.full[st], total);
         __syncwarp();
@@ -361,6 +362,7 @@ __device__ __forceinline__ void attn_feed(const AttnParams &p, const CacheMaps &
         }
         page = page_next;
         row = row_next;
+        wanted = wanted_next;
     }
 }
 

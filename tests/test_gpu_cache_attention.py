@@ -183,6 +183,26 @@ def test_many_sequences(fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("order", ["nhd", "hnd"])
+@pytest.mark.parametrize("n,lens", [(1, 300), (2, 9000), (60, 300)])
+@pytest.mark.parametrize("bad", [-1, -2, -3, 2 ** 31 - 1, -2 ** 31])
+def test_any_page_id_outside_reads_as_zeros(fmt, order, n, lens, bad):
+    """Negative ids and ids past the last page, in every kernel and scale layout."""
+    b = Batch(n=[n], lens=[lens], hq=4, hkv=2, D=64, page=16, fmt=fmt, order=order, seed=20,
+              poison=False)
+    b.k64 = torch.cat([b.k64, torch.zeros_like(b.k64[:1])])
+    b.v64 = torch.cat([b.v64, torch.zeros_like(b.v64[:1])])
+    where = [0, 3, 7, (lens - 1) // 16]
+    assert qkr.device_status(reset=True) == 0
+    b.table[0, where] = bad
+    b.call()
+    torch.cuda.synchronize()
+    assert qkr.device_status(reset=True) == 8
+    b.table[0, where] = 2 ** 30     # the definition clamps it to the page of zeros
+    b.check()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_bad_metadata_is_clamped_and_reported(fmt):
     """Lengths, offsets and page ids outside their bounds: no access outside the
     buffers, the other sequences as they should be, bit 8 of the status word."""
