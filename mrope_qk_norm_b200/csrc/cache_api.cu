@@ -305,7 +305,7 @@ qkr_status make_plan(const Sizes &s, int64_t page_size, Plan *plan)
         // SMs times what a CTA then does, its tiles and some 5 tiles' time of setting
         // up and writing out (20 of 3400 clocks a tile); joining parts costs 3 more.
         // A sequence's last block is counted half (four chunks of 300 to 512 tokens
-        // on 8192 cached in 4 bits: 142 us in 3 parts, 129 whole).
+        // on 8192 cached in 4 bits: 142 us in 3 parts, 129 whole; 106 since).
         const int64_t most_items = p.n_blocks * s.Hkv;
         int64_t items = (s.T * G / 256 + (s.B + 1) / 2) * s.Hkv;
         if (items > most_items)

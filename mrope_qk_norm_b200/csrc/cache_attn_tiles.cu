@@ -11,8 +11,8 @@
 // Two threads share a row, 64 scores each, because the softmax's latency is what
 // the tensor cores wait for; the two agree on the reference through a named
 // barrier.  The softmax warps take registers from the others
-// (setmaxnreg): 4 x 104 + 64 of the 5 x 96 launched (4 bits: 4 x 88 + 2 x 64 of
-// 6 x 80).
+// (setmaxnreg): 4 x 104 + 64 of the 5 x 96 launched (4 bits: 4 x 88 + 3 x 48 of
+// 7 x 72).
 //
 //   warps 0-15      softmax: 0-7 of tile 0, 8-15 of tile 1
 //   warp 16         issues the matrix instructions, in the order
@@ -20,8 +20,8 @@
 //                   softmax runs, the tensor cores work for the other
 //   bf16: 17, 18    K tiles, V tiles by TMA, a ring of 32 KB (16 KB) stages
 //         19        clears the values no row of the block sees (below)
-//   4 bits: 20-23   K and V tiles from nibbles to bf16 in shared memory, one
-//                   key a thread
+//   4 bits: 20-27   K tiles (20-23) and V tiles from nibbles to bf16 in shared
+//                   memory, one key a thread
 //
 // Per tile and 128 keys at D = 128 the two products take 1024 clocks of the
 // tensor cores and the 16384 exponentials 1024 clocks of the SM's exponential
@@ -58,7 +58,7 @@ namespace qkr {
 namespace {
 
 constexpr int kSoftWarps = 16;
-constexpr int tiles_threads(bool q4) { return 32 * (kSoftWarps + (q4 ? 8 : 4)); }
+constexpr int tiles_threads(bool q4) { return 32 * (kSoftWarps + (q4 ? 12 : 4)); }
 constexpr int kTile = 128;               // keys of a tile, rows of a tile
 constexpr float kSlack = 8.f;
 // One pair of exponentials in 8 on the FMA pipe (8192-token prompt: 251 us; every
@@ -685,7 +685,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             }
         }
     } else {
-    regs_down<64>();
+    regs_down<Q4 ? 48 : 64>();
     if (warp == kSoftWarps) {
         // ================================================ matrix instructions
         constexpr uint32_t kId = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(kTile / 16) << 24;
@@ -864,12 +864,12 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         }
     } else if (Q4 && warp >= kSoftWarps + 4) {
         // ================================================ 4 bits to bf16, one key a thread
-        const int row = threadIdx.x - 32 * (kSoftWarps + 4);
+        const int row = threadIdx.x & 127;
+        const bool is_v = warp >= kSoftWarps + 8;      // one warpgroup K, one V
         constexpr int GR = DP / 32;
         uint32_t code[4 * GR], sc[GR / 2];
         auto fetch = [&](int it) {
             const int j = k.tile_at(i0 + (it >> 1)) * kTile + row;
-            const bool is_v = it & 1;
 #pragma unroll
             for (int i = 0; i < 4 * GR; ++i)
                 code[i] = 0x88888888u;
@@ -903,10 +903,9 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         const bool mixed = k.p_first != k.p_last;
         bool ok = true;
         if (nt > 0)
-            fetch(0);
-        for (int it = 0; it < 2 * nt && ok; ++it) {
+            fetch(is_v);
+        for (int it = is_v; it < 2 * nt && ok; it += 2) {
             const int st = it % NST;
-            const bool is_v = it & 1;
             if (it >= NST) {
                 ok = bar_wait<kAhead>(&sh.empty[st], (it / NST - 1) & 1, &sh.abort);
                 if (!ok)
@@ -951,8 +950,8 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             }
             fence_async();
             bar_arrive(&sh.raw[st]);
-            if (it + 1 < 2 * nt)
-                fetch(it + 1);
+            if (it + 2 < 2 * nt)
+                fetch(it + 2);
         }
     }
     }
