@@ -386,3 +386,39 @@ def test_lse_is_optional_and_joins_two_caches():
     joined = sum(x.unsqueeze(-1) * p[0] for x, p in zip(w, parts))
     assert (joined - whole).abs().max() < 3 * 2 ** -8 * whole.abs().max()
     assert math.isfinite(float(joined.sum()))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_binding_refusals(fmt):
+    """What the binding itself refuses, before the library is called."""
+    b = Batch(n=[1, 2], lens=[40, 50], hq=4, hkv=2, D=64, page=16, fmt=fmt, seed=21)
+
+    def call(**kw):
+        a = dict(q=b.q, cache=b.cache, out=b.out, page_table=b.table, lens=b.lens, cu_q=b.cu,
+                 max_q=2, max_len=50)
+        a.update(kw)
+        qkr.cache_attention(**a)
+    call()
+    for kw in (dict(q=b.q.float()), dict(q=b.q.cpu()), dict(q=b.q[..., :32]), dict(q=b.q[0]),
+               dict(q=b.q.transpose(1, 2)), dict(out=b.out[:1]), dict(out=b.out.float()),
+               dict(out=b.out.transpose(0, 1)), dict(page_table=b.table.long()),
+               dict(page_table=b.table[:1]), dict(page_table=b.table.t().contiguous().t()),
+               dict(lens=b.lens.long()), dict(lens=b.lens[:1]), dict(cu_q=b.cu[:2]),
+               dict(cu_q=b.cu.cpu()), dict(max_len=16 * b.table.shape[1] + 1),
+               dict(lse=b.lse.half()), dict(lse=b.lse[:, :2])):
+        with pytest.raises(ValueError):
+            call(**kw)
+    with pytest.raises(qkr.QkrError) as e:
+        call(window=-1)
+    assert e.value.status == qkr.QKR_ERR_INVALID_ARG
+    big = Batch(n=[1] * 8, lens=[5000] * 8, hq=4, hkv=2, D=64, page=16, fmt=fmt, seed=22)
+    need = qkr.cache_attention_workspace(big.q, big.cache, 8, 1, 5000)
+    assert need > 0
+    with pytest.raises(qkr.QkrError) as e:
+        big.call(workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    assert "workspace" in str(e.value)
+    planes = b.planes
+    make = qkr.cache_desc if fmt == "bf16" else qkr.cache_desc_q4
+    for bad in (planes[0][0], planes[0].float(), planes[0].cpu(), planes[0][..., :-8]):
+        with pytest.raises(ValueError):
+            make(bad, *planes[1:])
