@@ -495,7 +495,8 @@ def _cache_common(fmt, k, D, tensors) -> CacheDesc:
     d.format = fmt
     d.n_pages, d.page_size, d.Hkv, d.D = k.shape[0], k.shape[1], k.shape[2], D
     d._keep = tensors  # the descriptor holds raw pointers into these
-    d._device, d._page, d._H, d._D = k.device, k.shape[1], k.shape[2], D
+    d._index, d._page, d._H, d._D = k.get_device(), k.shape[1], k.shape[2], D
+    d._scale = D ** -0.5 if D else 0.0
     return d
 
 
@@ -529,28 +530,22 @@ def cache_desc_q4(k, k_scale, v, v_scale) -> CacheDesc:
 # host side short: every property of a tensor is read once, and the device is
 # switched only when it is not the current one.
 
-def _launch(device, stream, fn, *args):
-    """fn(stream, *args) with `device` current, on `stream` or its current stream."""
-    i = device.index
+def _raw_stream(stream, index) -> int:
     if stream is None:
-        s = torch._C._cuda_getCurrentRawStream(i)
-    else:
-        s = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
-    if torch._C._cuda_getDevice() == i:
-        status = fn(s, *args)
-    else:
-        with torch.cuda.device(i):
-            status = fn(s, *args)
-    if status != QKR_OK:
-        _check(status)
+        return torch._C._cuda_getCurrentRawStream(index)
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _arg(t, dtype, device, what) -> int:
+def _call_on(index, fn, *args):
+    """fn(*args) with device `index` current (it is not)."""
+    with torch.cuda.device(index):
+        return fn(*args)
+
+
+def _wrong(t, dtype, index, what):
     if t.dtype is not dtype:
         raise ValueError("%s must be %s, got %s" % (what, dtype, t.dtype))
-    if t.get_device() != device.index:
-        raise ValueError("%s must be on the cache's device %s" % (what, device))
-    return t.data_ptr()
+    raise ValueError("%s must be on the cache's device cuda:%d, got %s" % (what, index, t.device))
 
 
 def cache_attention_workspace(q, cache: CacheDesc, batch, max_q, max_len, window=0,
@@ -558,8 +553,10 @@ def cache_attention_workspace(q, cache: CacheDesc, batch, max_q, max_len, window
     """Bytes of workspace cache_attention needs for q [T, Hq, D] and these sizes."""
     n = ctypes.c_int64(0)
     T, Hq, _ = q.shape
-    _launch(cache._device, None, lambda s, *a: _lib.cache_attention_workspace(*a), ctypes.byref(cache), T,
-            Hq, batch, max_q, max_len, window, n_sink, ctypes.byref(n))
+    args = (ctypes.byref(cache), T, Hq, batch, max_q, max_len, window, n_sink, ctypes.byref(n))
+    fn = _lib.cache_attention_workspace
+    at = cache._index
+    _check(fn(*args) if torch._C._cuda_getDevice() == at else _call_on(at, fn, *args))
     return int(n.value)
 
 
@@ -571,26 +568,26 @@ def cache_attention(q, cache: CacheDesc, out, page_table, lens, cu_q, max_q, max
     [B], cu_q int32 [B + 1]; lse: fp32 [T, Hq] or None; workspace: uint8, at least
     cache_attention_workspace(...) bytes (None where that is 0); scale defaults to
     D ** -0.5.  include/qkr.h states what a token sees."""
-    dev = cache._device
-    D = cache._D
-    qs, os_ = q.shape, out.shape
-    if len(qs) != 3 or qs[2] != D:
+    at, D = cache._index, cache._D
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != D:
         raise ValueError("q must be [T, Hq, %d] with a contiguous last dim" % D)
-    T, Hq, _ = qs
+    T, Hq, _ = shape
     qt, qh, qd = q.stride()
     if qd != 1:
         raise ValueError("q must be [T, Hq, %d] with a contiguous last dim" % D)
-    if os_ != qs:
+    if out.shape != shape:
         raise ValueError("out must have q's shape and dense heads")
     ot, oh, od = out.stride()
     if od != 1 or (Hq > 1 and oh != D):
         raise ValueError("out must have q's shape and dense heads")
-    ls, cs, ts = lens.shape, cu_q.shape, page_table.shape
-    if len(ls) != 1 or len(cs) != 1 or len(ts) != 2 or cs[0] != ls[0] + 1 or ts[0] != ls[0]:
+    if page_table.dim() != 2 or lens.dim() != 1 or cu_q.dim() != 1:
         raise ValueError("lens must be [B], cu_q [B + 1], page_table [B, pages]")
-    B, cols = ts
+    B, cols = page_table.shape
+    if lens.numel() != B or cu_q.numel() != B + 1:
+        raise ValueError("lens must be [B], cu_q [B + 1], page_table [B, pages]")
     tb, tc = page_table.stride()
-    if (B > 1 and lens.stride(0) != 1) or cu_q.stride(0) != 1 or (cols > 1 and tc != 1):
+    if not lens.is_contiguous() or not cu_q.is_contiguous() or (cols > 1 and tc != 1):
         raise ValueError("lens, cu_q and the rows of page_table must be contiguous")
     if B > 1:
         if tb < cols:
@@ -601,40 +598,58 @@ def cache_attention(q, cache: CacheDesc, out, page_table, lens, cu_q, max_q, max
         raise ValueError("max_len %d exceeds the %d tokens of a page_table row"
                          % (max_len, cols * cache._page))
     i32, bf = torch.int32, torch.bfloat16
+    for t, dtype, what in ((q, bf, "q"), (out, bf, "out"), (page_table, i32, "page_table"),
+                           (lens, i32, "lens"), (cu_q, i32, "cu_q")):
+        if t.dtype is not dtype or t.get_device() != at:
+            _wrong(t, dtype, at, what)
     lse_p = ws_p = ws_n = 0
     if lse is not None:
-        if lse.shape != qs[:2] or not lse.is_contiguous():
+        if lse.shape != shape[:2] or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous [T, Hq] tensor")
-        lse_p = _arg(lse, torch.float32, dev, "lse")
+        if lse.dtype is not torch.float32 or lse.get_device() != at:
+            _wrong(lse, torch.float32, at, "lse")
+        lse_p = lse.data_ptr()
     if workspace is not None:
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
+        if workspace.get_device() != at:
+            _wrong(workspace, workspace.dtype, at, "workspace")
         ws_n = workspace.nbytes
-        ws_p = _arg(workspace, workspace.dtype, dev, "workspace")
-    _launch(dev, stream, _lib.cache_attention, ctypes.byref(cache), _arg(q, bf, dev, "q"),
-            _arg(out, bf, dev, "out"), lse_p, T, Hq, qt, qh if Hq > 1 else D,
-            ot if T > 1 else Hq * D, _arg(page_table, i32, dev, "page_table"), tb,
-            _arg(lens, i32, dev, "lens"), _arg(cu_q, i32, dev, "cu_q"), B, max_q, max_len,
-            D ** -0.5 if scale is None else scale, window, n_sink, ws_p, ws_n)
+        ws_p = workspace.data_ptr()
+    args = (_raw_stream(stream, at), ctypes.byref(cache), q.data_ptr(), out.data_ptr(), lse_p, T, Hq,
+            qt, qh if Hq > 1 else D, ot if T > 1 else Hq * D, page_table.data_ptr(), tb,
+            lens.data_ptr(), cu_q.data_ptr(), B, max_q, max_len,
+            cache._scale if scale is None else scale, window, n_sink, ws_p, ws_n)
+    fn = _lib.cache_attention
+    status = fn(*args) if torch._C._cuda_getDevice() == at else _call_on(at, fn, *args)
+    if status != QKR_OK:
+        _check(status)
 
 
 def _rows_q4(fn, k, v, cache, row_idx, stream):
-    dev, H, D = cache._device, cache._H, cache._D
-    ks, vs, n = k.shape, v.shape, row_idx.shape
-    if len(ks) != 3 or ks[1] != H or ks[2] != D or vs != ks or len(n) != 1 or n[0] != ks[0]:
+    at, H, D = cache._index, cache._H, cache._D
+    shape = k.shape
+    if len(shape) != 3 or shape[1] != H or shape[2] != D or v.shape != shape or \
+            row_idx.dim() != 1 or row_idx.numel() != shape[0]:
         raise ValueError("k and v must be [T, %d, %d], row_idx [T]" % (H, D))
-    T = ks[0]
+    T = shape[0]
     kt, kh, kd = k.stride()
     vt, vh, vd = v.stride()
     if kd != 1 or vd != 1 or (H > 1 and (kh != D or vh != D)):
         raise ValueError("k and v must have dense heads")
-    if T > 1 and row_idx.stride(0) != 1:
+    if not row_idx.is_contiguous():
         raise ValueError("row_idx must be contiguous")
     if T <= 1:
         kt = vt = H * D
     bf = torch.bfloat16
-    _launch(dev, stream, fn, ctypes.byref(cache), _arg(k, bf, dev, "k"), _arg(v, bf, dev, "v"),
-            _arg(row_idx, torch.int64, dev, "row_idx"), T, kt, vt)
+    for t, dtype, what in ((k, bf, "k"), (v, bf, "v"), (row_idx, torch.int64, "row_idx")):
+        if t.dtype is not dtype or t.get_device() != at:
+            _wrong(t, dtype, at, what)
+    args = (_raw_stream(stream, at), ctypes.byref(cache), k.data_ptr(), v.data_ptr(),
+            row_idx.data_ptr(), T, kt, vt)
+    status = fn(*args) if torch._C._cuda_getDevice() == at else _call_on(at, fn, *args)
+    if status != QKR_OK:
+        _check(status)
 
 
 def cache_set_rows_q4(k, v, cache: CacheDesc, row_idx, stream=None):
