@@ -490,7 +490,7 @@ qkr_status cache_attention_workspace(const qkr_cache_desc *cache, int64_t T, int
  * infinity or a NaN reads back as NaN throughout.
  *
  *   k, v             bf16 device [T, Hkv, D], heads dense, token strides in
- *                    elements (multiples of 8), 16-byte aligned.
+ *                    elements (multiples of 8), 16-byte aligned; T * Hkv <= 2^30.
  *   row_idx          int64 device [T], 8-byte aligned; rows must be distinct
  *                    within a call.  A row outside the cache is not written and
  *                    raises bit 4 of the device status word.

@@ -510,8 +510,8 @@ static qkr_status rows_q4(void *stream, const qkr_cache_desc *cache, const void 
         return api_fail(QKR_ERR_INVALID_ARG, "T must be >= 0");
     if (T == 0)
         return api_done(qkr::LaunchRecord());
-    if (T > INT_MAX || T * cache->Hkv > ((int64_t)1 << 34))
-        return api_fail(QKR_ERR_UNSUPPORTED, "T < 2^31 and T * Hkv <= 2^34");
+    if (T > INT_MAX || T * cache->Hkv > ((int64_t)1 << 30))
+        return api_fail(QKR_ERR_UNSUPPORTED, "need T * Hkv <= 2^30");
     if (!k || !v || !row_idx)
         return api_fail(QKR_ERR_INVALID_ARG, "k, v and row_idx must be non-NULL");
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(row_idx, 8))

@@ -35,20 +35,27 @@ struct Where {
     bool inside;
 };
 
+// (32-bit divisions: T * Hkv <= 2^30, and few caches have 2^32 rows.)
 __device__ __forceinline__ bool locate(const RowsQ4 &p, Where *w)
 {
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     w->lane4 = (int)(i & 3);
-    const int64_t r = i >> 2;
-    w->head = (int)(r % p.c.Hkv);
-    w->which = (int)(r / p.c.Hkv & 1);
-    w->t = r / p.c.Hkv >> 1;
+    const uint32_t r = (uint32_t)(i >> 2), H = (uint32_t)p.c.Hkv, th = r / H;
+    w->head = (int)(r - th * H);
+    w->which = (int)(th & 1);
+    w->t = th >> 1;
     if (w->t >= p.T)
         return false;
     const int64_t at = p.rows[w->t];
+    const uint32_t ps = (uint32_t)p.c.page_size;
     w->inside = at >= 0 && at < (int64_t)p.c.n_pages * p.c.page_size;
-    w->page = at / p.c.page_size;
-    w->row = (int)(at % p.c.page_size);
+    if ((uint64_t)at >> 32 == 0) {
+        w->page = (uint32_t)at / ps;
+        w->row = (int)((uint32_t)at % ps);
+    } else {
+        w->page = at / p.c.page_size;
+        w->row = (int)(at % p.c.page_size);
+    }
     if (!w->inside && w->lane4 == 0 && w->head == 0)
         atomicOr(p.status, kStatusRow);
     return true;
