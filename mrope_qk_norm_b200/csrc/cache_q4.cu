@@ -75,16 +75,16 @@ __device__ __forceinline__ float group_scale(float hi, float lo)
     return fminf(fmaxf(s, -31.f * 0x1p120f), 31.f * 0x1p120f);
 }
 
-// clamp(rint(x / s), -8, 7) + 8 from r = 1/s rounded.  x r is within 2^-21 of x / s;
-// adding 1536 rounds it to a multiple of 2^-13.  x has 8 significant bits and s 5,
-// so a quotient that is not half way between two codes is at least 2^-5 / 62 from
-// it, and one that is becomes exactly that: rint sees the true side and the true
-// ties (to even).  The last addition leaves the code in the low bits.
+// min(rint(x / s), 7) + 8 from r = 1/s rounded (never below 0: s is rounded up, or
+// at its largest still above x / 8.5).  x r is within 2^-21 of x / s; adding 1536
+// rounds it to a multiple of 2^-13.  x has 8 significant bits and s 5, so a quotient
+// that is not half way between two codes is at least 2^-5 / 62 from it, and one
+// that is becomes exactly that: the rounding below sees the true side and the true
+// ties (to even).  It leaves the code in the low bits of 1.5 * 2^23 + code.
 __device__ __forceinline__ uint32_t code_of(float x, float r)
 {
-    float t = fmaf(x, r, 1536.f) - 1536.f;
-    t = fminf(fmaxf(t, -8.f), 7.f);
-    return __float_as_uint(t + 12582920.f) & 15u;
+    const float t = fminf(fmaf(x, r, 1536.f), 1543.f);
+    return __float_as_uint(t + 12581384.f) & 15u;      // 12582912 + 8 - 1536
 }
 
 template <int D>

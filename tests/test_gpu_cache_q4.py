@@ -94,6 +94,35 @@ def test_ties_zeros_and_extremes():
     assert (err <= x.double().abs()[[5, 6, 10]] / 8 + 2.0 ** -126).all()
 
 
+def test_every_mantissa_against_every_scale():
+    """Each of the 16 scale mantissas with every bf16 mantissa at every exponent
+    whose quotient can reach half a code, both signs: all quotients and ties there
+    are (up to a common power of two)."""
+    D, groups = 128, []
+    x = torch.tensor([sign * m * 2.0 ** e for e in range(-12, 1) for m in range(128, 256)
+                      for sign in (1.0, -1.0)])
+    for mant in range(16, 32):
+        for extreme in (-8.0 * mant, 8.0 * mant):
+            v = x[(x.abs() <= 8 * mant) & (x != -extreme)]
+            pad = (-len(v)) % 31
+            v = torch.cat([v, torch.zeros(pad)]).view(-1, 31)
+            groups.append(torch.cat([torch.full((len(v), 1), extreme), v], 1))
+    g = torch.cat(groups)
+    g = torch.cat([g, torch.zeros(-len(g) % (D // 32), 32)])
+    T = g.numel() // D
+    k = g.view(T, 1, D).to(torch.bfloat16).cuda()
+    assert (k.float().cpu().view(-1) == g.view(-1)).all()
+    page = 64
+    planes = _planes((T + page - 1) // page, page, 1, D)
+    cache = qkr.cache_desc_q4(*planes)
+    rows = torch.arange(T, device="cuda")
+    qkr.cache_set_rows_q4(k, k, cache, rows)
+    c, sc = quantise64(k)
+    assert torch.equal(planes[0].view(-1, 1, D // 2)[:T], pack(c, False))
+    assert torch.equal(planes[2].view(-1, 1, D // 2)[:T], pack(c, True))
+    assert torch.equal(_bits(planes[1].view(-1, 1, D // 32)[:T]), _bits(sc.to(torch.bfloat16)))
+
+
 def test_nonfinite_groups_read_back_as_nan():
     x = torch.ones((3, 2, 128), dtype=torch.bfloat16, device="cuda")
     x[0, 0, 40] = float("inf")
