@@ -459,7 +459,8 @@ typedef struct qkr_cache_desc {
  * [0, max_len], a cu_q entry outside [0, T], or more than max_q new tokens is
  * clamped, a page id outside the cache reads as rows of zeros, and each raises
  * bit 8 of the device status word.
- * The maximum, the sum and the output are held in fp32; the weights exp(s - m)
+ * The maximum, the sum and the output are held in fp32 and divided at the end, so
+ * seen values of V beyond 2^100 in magnitude can overflow; the weights exp(s - m)
  * are rounded to bf16 for their product with V, and out once at the end.
  * Enqueues one kernel for sequences of few rows (new tokens times query heads of a
  * KV head, up to 16) or of many, or one for each where both can stand side by
