@@ -568,8 +568,10 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                 tc_fence_before();
                 bar_arrive(&sh.p_full[h]);
             }
-            if (nt > 0)
-                bar_wait(&sh.o_full[h], 0, &sh.abort);
+            // Q's tile is written over below: not before the products have read it, and
+            // where there are none (no key is seen) not before every warp has stored its
+            // rows of it (at D <= 64 a warp's share holds another pair's rows)
+            bar_wait(nt > 0 ? &sh.o_full[h] : &sh.q_full, 0, &sh.abort);
             tc_fence_after();
             const bool only = nparts == 1;
             // both halves' sums, and one decision for both
