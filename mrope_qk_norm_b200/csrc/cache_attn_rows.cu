@@ -117,7 +117,7 @@ struct alignas(16) RowsShared {
     float o[kWarps][8 * NT][DP + 4];
     float m[kWarps][8 * NT], l[kWarps][8 * NT];
     int poison, abort;
-    int scan[kWarps + 1];
+    int64_t scan[kWarps + 1];
     uint64_t full[4], empty[4];
 };
 
@@ -896,8 +896,9 @@ attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
                    ? p.piece_cost + max(1, attn_block_at(p, b, 0, n, t0, bad).ntiles)
                    : 0;
     };
-    // inclusive sum over the CTA's threads, and the total
-    auto scan = [&](int v, int *total) -> int {
+    // inclusive sum over the CTA's threads, and the total.  A sequence has at most 2^25
+    // tiles (2^29 keys of 16) and its piece_cost: 32 of them fit 32 bits, 160 do not.
+    auto scan = [&](int v, int64_t *total) -> int64_t {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int up = __shfl_up_sync(0xffffffffu, v, o);
@@ -908,7 +909,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
         if (lane == 31)
             sh.scan[warp] = v;
         __syncthreads();
-        int add = 0, all = 0;
+        int64_t add = 0, all = 0;
 #pragma unroll
         for (int w = 0; w < kWarps + 1; ++w) {
             add += w < warp ? sh.scan[w] : 0;
@@ -917,10 +918,10 @@ attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
         *total = all;
         return v + add;
     };
-    int64_t all_tiles = 0;
-    int mine = 0, upto = 0;        // of the chunk of sequences looked at last
+    int64_t all_tiles = 0, upto = 0;
+    int mine = 0;                  // of the chunk of sequences looked at last
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-        int total;
+        int64_t total;
         mine = tiles_of(b0 + threadIdx.x);
         upto = scan(mine, &total);
         all_tiles += total;
@@ -940,12 +941,12 @@ attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
     int64_t before = 0;
     int b = -1;
     for (int b0 = 0; b < 0; b0 += kThreads) {
-        int total;
+        int64_t total;
         if (p.B > kThreads) {
             mine = tiles_of(b0 + threadIdx.x);
             upto = scan(mine, &total);
         } else {
-            total = (int)all_tiles;
+            total = all_tiles;
         }
         if (at < (before + total) * Hkv) {
             const int64_t hi = (before + upto) * Hkv, lo = hi - (int64_t)mine * Hkv;
@@ -955,7 +956,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
                 sh.scan[1] = upto - mine;
             }
             __syncthreads();
-            b = sh.scan[0];
+            b = (int)sh.scan[0];
             before += sh.scan[1];
         } else {
             before += total;
