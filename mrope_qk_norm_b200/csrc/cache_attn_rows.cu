@@ -299,9 +299,12 @@ __device__ __forceinline__ void attn_feed(const AttnParams &p, const CacheMaps &
         __syncwarp();
         const bool by_bulk = !scales || p.dense_scales;
         const bool issue = by_bulk && wanted && (page >= 0 || !scales);
-        if (wanted && scales && p.dense_scales && page < 0)
+        if (wanted && scales && p.dense_scales && page < 0) {
             for (int x = 0; x < (int)bytes; x += 16)
                 *reinterpret_cast<uint4 *>(ring + st * R::kStageBytes + to + x) = make_uint4(0, 0, 0, 0);
+            // the stage's next fill may copy over these zeros: not before they are there
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
         uint32_t total = issue ? bytes : 0;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)

@@ -50,3 +50,26 @@ def test_most_tiles_a_batch_can_have():
     # a sum of 2^29 ones: ln(2^29) to fp32's accuracy
     assert (lse.double() - 29 * 0.6931471805599453).abs().max() < 20.2 * 2.0 ** -22
     assert qkr.device_status(reset=True) == 0
+
+
+@pytest.mark.parametrize("order", ["nhd", "hnd"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("n,lens", [([1], [2500]), ([1] * 3, [9000, 5000, 3000])])
+def test_pages_outside_the_cache_among_others(order, D, page, n, lens):
+    """4-bit rows: every second or third page reads as zeros, so that stages of the
+    ring are zeroed and copied into by turns."""
+    b = Batch(n=n, lens=lens, hq=4, hkv=2, D=D, page=page, fmt="q4", order=order, seed=32,
+              poison=False)
+    b.k64 = torch.cat([b.k64, torch.zeros_like(b.k64[:1])])
+    b.v64 = torch.cat([b.v64, torch.zeros_like(b.v64[:1])])
+    assert qkr.device_status(reset=True) == 0
+    b.table[:, ::2] = 2 ** 30       # the definition clamps it to the page of zeros
+    b.table[:, 1::3] = 2 ** 30
+    for _ in range(3):
+        b.out_buf.fill_(7.0)
+        b.lse.fill_(7.0)
+        b.call()
+        torch.cuda.synchronize()
+        b.check()
+    assert qkr.device_status(reset=True) == 8
