@@ -64,11 +64,12 @@ __device__ float cached(const CachePlane &pl, const CachePlane &sc, int page, in
 // lane sums o for its DP/32 dims.  A key the row does not see is skipped, so
 // nothing it holds can reach the row; the blocks whose values hold an infinity
 // or a NaN in a key that only some of their rows see take this path, because in
-// a matrix product 0 * NaN is NaN.  Slow and rare.
+// a matrix product 0 * NaN is NaN.  Slow and rare: some microseconds a key.  `beat`
+// (or null) is counted up once a tile, for whoever waits meanwhile.
 template <int DP, bool Q4>
 __device__ __noinline__ void attn_row_exact(const AttnParams &p, const AttnBlock &k, int kvh,
                                             int r, int i0, int i1, float *m_out, float *l_out,
-                                            float (&o)[DP / 32])
+                                            float (&o)[DP / 32], int *beat)
 {
     constexpr int E = DP / 32;
     const int lane = threadIdx.x & 31;
@@ -86,6 +87,8 @@ __device__ __noinline__ void attn_row_exact(const AttnParams &p, const AttnBlock
     float m = -INFINITY, l = 0.f;
     for (int i = i0; i < i1; ++i) {
         const int j0 = k.tile_at(i) * p.tile;
+        if (beat && lane == 0)
+            atomicAdd(beat, 1);
         for (int j = j0; j < j0 + p.tile; ++j) {
             if (!attn_sees(p, pos, j))
                 continue;

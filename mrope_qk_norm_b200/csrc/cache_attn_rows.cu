@@ -66,8 +66,8 @@ namespace {
 
 constexpr int kWarps = 4;              // computing warps; one more feeds them
 constexpr int kThreads = 32 * (kWarps + 1);
-// A wait asks so often at most.  Roles that run ahead sleep in between (their polls
-// would take issue slots from the others).
+// A wait asks so often at most, 8.6 s (an asking that fails takes some 4 us).  Roles that
+// run ahead sleep in between (their polls would take issue slots from the others).
 constexpr uint32_t kWaitLimit = 1u << 21;
 constexpr uint32_t kMinus136 = 0xc308c308u;  // bf16 pair
 constexpr float kSlack = 8.f;  // log2 units the reference may lag behind the maximum
@@ -117,6 +117,7 @@ struct alignas(16) RowsShared {
     float o[kWarps][8 * NT][DP + 4];
     float m[kWarps][8 * NT], l[kWarps][8 * NT];
     int poison, abort;
+    int beat;                  // counted up where rows are computed key by key
     int64_t scan[kWarps + 1];
     uint64_t full[4], empty[4];
 };
@@ -182,9 +183,14 @@ __device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity)
     return ok != 0;
 }
 // Bounded; after a wait that ran out no other waits (the result is reported as
-// not valid, nothing is accessed that would not be otherwise).
-__device__ __noinline__ void bar_wait_long(uint64_t *bar, uint32_t parity, int *abort, int sleep)
+// not valid, nothing is accessed that would not be otherwise).  Where `beat` is
+// given the count starts again whenever that moves: the computing warps free no stage
+// while they go through a piece key by key (16 rows: 2 us a key, so that the limit alone
+// would allow some 4 million keys).
+__device__ __noinline__ void bar_wait_long(uint64_t *bar, uint32_t parity, int *abort, int sleep,
+                                           const int *beat)
 {
+    int last = beat ? *reinterpret_cast<const volatile int *>(beat) : 0;
     for (uint32_t i = 0; i < kWaitLimit; ++i) {
         if (bar_try(bar, parity))
             return;
@@ -192,13 +198,18 @@ __device__ __noinline__ void bar_wait_long(uint64_t *bar, uint32_t parity, int *
             return;
         if (sleep)
             __nanosleep(sleep);
+        if (beat && *reinterpret_cast<const volatile int *>(beat) != last) {
+            last = *reinterpret_cast<const volatile int *>(beat);
+            i = 0;
+        }
     }
     *reinterpret_cast<volatile int *>(abort) = 1;
 }
-__device__ __forceinline__ void bar_wait(uint64_t *bar, uint32_t parity, int *abort, int sleep = 0)
+__device__ __forceinline__ void bar_wait(uint64_t *bar, uint32_t parity, int *abort, int sleep = 0,
+                                         const int *beat = nullptr)
 {
     if (!__all_sync(0xffffffffu, bar_try(bar, parity)))
-        bar_wait_long(bar, parity, abort, sleep);
+        bar_wait_long(bar, parity, abort, sleep, beat);
 }
 
 // A warp's place in the ring.
@@ -295,7 +306,7 @@ __device__ __forceinline__ void attn_feed(const AttnParams &p, const CacheMaps &
             page = -1;      // reads as zeros
         }
         // (the stages' first use finds the phase before the first complete)
-        bar_wait(&sh.empty[st], at->phase ^ 1u, &sh.abort, 100);
+        bar_wait(&sh.empty[st], at->phase ^ 1u, &sh.abort, 100, &sh.beat);
         __syncwarp();
         const bool by_bulk = !scales || p.dense_scales;
         const bool issue = by_bulk && wanted && (page >= 0 || !scales);
@@ -754,6 +765,7 @@ __device__ __forceinline__ void rows_setup(RowsShared<DP, NT> &sh, int fills)
         }
         sh.poison = 0;
         sh.abort = 0;
+        sh.beat = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -762,7 +774,7 @@ __device__ __forceinline__ void rows_setup(RowsShared<DP, NT> &sh, int fills)
 // Row r of the piece: the warps' parts joined, in fixed order.
 template <int DP, int NT, bool Q4>
 __device__ __forceinline__ void attn_piece_row(const AttnParams &p, const AttnBlock &k, int kvh,
-                                               int i0, int i1, const RowsShared<DP, NT> &sh, int r,
+                                               int i0, int i1, RowsShared<DP, NT> &sh, int r,
                                                float *m, float *l, float (&acc)[DP / 32])
 {
     constexpr int E = DP / 32;
@@ -770,7 +782,7 @@ __device__ __forceinline__ void attn_piece_row(const AttnParams &p, const AttnBl
     *m = -INFINITY;
     *l = 0.f;
     if (sh.poison) {
-        attn_row_exact<DP, Q4>(p, k, kvh, r, i0, i1, m, l, acc);
+        attn_row_exact<DP, Q4>(p, k, kvh, r, i0, i1, m, l, acc, &sh.beat);
         return;
     }
     float M = -INFINITY, L = 0.f;
@@ -1047,7 +1059,8 @@ attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
             before += cost;
             ++b;
         }
-    }    if (feeds)
+    }
+    if (feeds)
         feed_end(sh, it);
     else if (threadIdx.x == 0 && sh.abort)
         atomicOr(p.status, kStatusWait);

@@ -67,8 +67,8 @@ constexpr int kPolyEvery = 8;
 constexpr float kExpC0 = 0.9999992847442627f, kExpC1 = 0.6931217908859253f,
                 kExpC2 = 0.240247443318367f, kExpC3 = 0.05591785907745361f,
                 kExpC4 = 0.009570100344717503f;
-// A wait asks so often at most.  Roles that run ahead sleep in between (their polls
-// would take issue slots from the others).
+// A wait asks so often at most, 8.6 s (an asking that fails takes some 4 us).  Roles that
+// run ahead sleep in between (their polls would take issue slots from the others).
 constexpr uint32_t kWaitLimit = 1u << 21;
 constexpr int kAhead = 200;              // ns
 
@@ -583,7 +583,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             if (sh.sick[warp] | sh.sick[warp ^ 4]) {
                 for (int rr = r_warp + 16 * q; rr < min(r_warp + 16 * q + 16, k.nrows); ++rr) {
                     float pm, pl, po[E];
-                    attn_row_exact<DP, Q4>(p, k, kvh, rr, i0, i0 + nt, &pm, &pl, po);
+                    attn_row_exact<DP, Q4>(p, k, kvh, rr, i0, i0 + nt, &pm, &pl, po, nullptr);
                     attn_emit<E>(p, k, kvh, rr, part, only, pm, pl, po);
                 }
             } else {

@@ -73,3 +73,50 @@ def test_pages_outside_the_cache_among_others(order, D, page, n, lens):
         torch.cuda.synchronize()
         b.check()
     assert qkr.device_status(reset=True) == 8
+
+
+def test_long_piece_key_by_key():
+    """An infinite value that only the last token of a sequence sees sends a CTA's whole
+    piece, some 200,000 keys of 16 rows, through the key-by-key path (some 0.4 s).  The
+    next sequence's piece of the same CTA comes out as if nothing had happened, and no
+    bounded wait runs out."""
+    D, page, L, G, n = 64, 64, 1 << 25, 8, 2
+    P = 512                                     # pages in turn, L / (64 P) times over
+    g = torch.Generator().manual_seed(33)
+    v = torch.randint(-8, 25, (P + 2, page, 1, D), generator=g).to(torch.bfloat16)
+    v[P] = v[P - 1]                             # the sequences' last pages, of their own
+    v[P + 1] = v[P - 1]
+    v[P, page - 1, 0, 3] = float("inf")
+    k = torch.randn((P + 2, page, 1, D), generator=g).to(torch.bfloat16)
+    cache = qkr.cache_desc(k.cuda(), v.cuda())
+    table = (torch.arange(L // page) % P).to(torch.int32).repeat(2, 1)
+    table[0, -1], table[1, -1] = P, P + 1
+    # zero queries: every weight is one, and the sums are exact but for the joins
+    q = torch.zeros((2 * n, G, D), dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 7.0)
+    lens = torch.full((2,), L, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+    ws = torch.empty(qkr.cache_attention_workspace(q, cache, 2, n, L), dtype=torch.uint8,
+                     device="cuda")
+    assert qkr.device_status(reset=True) == 0
+    qkr.cache_attention(q, cache, out, table.cuda(), lens, cu, n, L, workspace=ws)
+    torch.cuda.synchronize()
+    assert qkr.device_status(reset=True) == 0
+    # the CTA in question ends the first sequence and begins the second
+    ctas, cost = qkr.last_launch()["grid"], L // 64 + 2
+    quota = -(-2 * cost // ctas)
+    assert cost % quota > quota // 2 and quota - cost % quota > 16
+    total = v[:P].double().sum((0, 1))[0] * (L // (64 * P))
+    last = v[P - 1, page - 1, 0].double()
+    # half a step of bf16, and a rounding of fp32 for each of at most `ctas` parts joined
+    rel = 2.0 ** -8 + 2 * ctas * 2.0 ** -24
+    for s in range(2):
+        for i in range(n):
+            want = (total if i else total - last) / (L - n + 1 + i)
+            got = out[s * n + i].double().cpu()
+            if s == 0 and i == 1:
+                assert torch.isposinf(got[:, 3]).all()
+                got[:, 3] = want[3]
+            # the numerators' parts are as large as the sum of magnitudes
+            size = v[:P].double().abs().mean((0, 1))[0]
+            assert ((got - want).abs() <= want.abs() * 2.0 ** -8 + size * (rel - 2.0 ** -8)).all()
