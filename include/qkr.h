@@ -457,7 +457,7 @@ typedef struct qkr_cache_desc {
  *                    streams, graphs replayed side by side) need one each.
  * What the host cannot see is bounded on the device: a length outside
  * [0, max_len], a cu_q entry outside [0, T], or more than max_q new tokens is
- * clamped, a page id outside the cache reads as rows of zeros, and each raises
+ * clamped, a cu_q entry below the one before it leaves a sequence no new tokens, a page id outside the cache reads as rows of zeros, and each raises
  * bit 8 of the device status word.
  * The maximum, the sum and the output are held in fp32 and divided at the end, so
  * seen values of V beyond 2^100 in magnitude can overflow; the weights exp(s - m)

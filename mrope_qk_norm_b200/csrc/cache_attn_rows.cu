@@ -907,6 +907,8 @@ attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
         int64_t t0;
         bool bad;
         const int n = attn_seq(p, b, &t0, &bad);
+        if (blockIdx.x == 0)
+            attn_report(p, b, bad);
         return attn_blocks_of(p, n)
                    ? p.piece_cost + max(1, attn_block_at(p, b, 0, n, t0, bad).ntiles)
                    : 0;

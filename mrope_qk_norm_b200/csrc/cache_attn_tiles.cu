@@ -374,6 +374,15 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
+    // metadata of sequences that attn_block need not have come by, 32 a CTA
+    if (warp == kSoftWarps + 3 && !p.direct && p.rows_lo == 0)
+        for (int64_t b = (int64_t)x * 32 + lane; b < p.B; b += (int64_t)gridDim.x * 32) {
+            int64_t t0;
+            bool bad;
+            attn_seq(p, (int)b, &t0, &bad);
+            attn_report(p, (int)b, bad);
+        }
+    __syncwarp();
     if (!used) {
         if (warp == kSoftWarps)
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));

@@ -101,6 +101,15 @@ __device__ __forceinline__ int attn_seq(const AttnParams &p, int b, int64_t *t0,
     return attn_clamp(p, p.cu[b], p.cu[b + 1], t0, bad);
 }
 
+// Raises the status bit if sequence b's offsets or length are outside their bounds.
+// (attn_block_of does it for a sequence with blocks; clamping may leave none.)
+__device__ __forceinline__ void attn_report(const AttnParams &p, int b, bool bad)
+{
+    const int L = p.lens[b];
+    if (bad || L < 0 || L > p.max_len)
+        atomicOr(p.status, kStatusBounds);
+}
+
 __device__ __forceinline__ int attn_blocks_of(const AttnParams &p, int n)
 {
     const int64_t r = (int64_t)n * p.G;
@@ -145,7 +154,8 @@ __device__ __forceinline__ AttnBlock attn_block_at(const AttnParams &p, int b, i
 
 // The block of block index `idx`, computed by a whole warp.  Where the blocks
 // are not laid out per sequence, each lane counts those of one sequence and
-// the warp adds them up, 32 sequences at a time.
+// the warp adds them up, 32 sequences at a time.  (Of sequences without blocks only
+// those laid out per sequence are reported here.)
 __device__ __forceinline__ AttnBlock attn_block(const AttnParams &p, uint32_t idx)
 {
     AttnBlock none = {};
@@ -158,8 +168,11 @@ __device__ __forceinline__ AttnBlock attn_block(const AttnParams &p, uint32_t id
         blk = (int)(idx % (uint32_t)p.blocks_max);
         n_of = attn_seq(p, b, &t0_of, &bad);
         nblk = attn_blocks_of(p, n_of);
-        if (blk >= nblk)
+        if (blk >= nblk) {
+            if (blk == 0 && (threadIdx.x & 31) == 0)
+                attn_report(p, b, bad);
             return none;
+        }
     } else {
         const int lane = threadIdx.x & 31;
         int64_t before = 0;

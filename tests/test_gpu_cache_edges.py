@@ -120,3 +120,43 @@ def test_long_piece_key_by_key():
             # the numerators' parts are as large as the sum of magnitudes
             size = v[:P].double().abs().mean((0, 1))[0]
             assert ((got - want).abs() <= want.abs() * 2.0 ** -8 + size * (rel - 2.0 ** -8)).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("what", ["past", "wholly_past", "negative", "decreasing", "long_empty",
+                                  "negative_empty"])
+@pytest.mark.parametrize("kernel", ["cluster", "shares", "tiles", "mixed"])
+def test_metadata_that_leaves_no_rows_is_reported(kernel, what, fmt):
+    """Offsets and lengths outside their bounds raise bit 8 also where clamping leaves
+    the sequence no tokens; the others are as they should be."""
+    n = [0] + {"cluster": [1, 1], "shares": [1, 2], "tiles": [70, 3], "mixed": [1, 70]}[kernel] + [0, 0]
+    lens = [5] + ([9000, 300] if kernel == "shares" else [300, 200]) + [7, 0]
+    b = Batch(n=n, lens=lens, hq=24 if kernel == "tiles" else 4, hkv=1, D=64, page=16, fmt=fmt,
+              seed=34, poison=False, pad=0)
+    most, longest = max(n), max(lens)
+
+    def check():
+        b.out_buf.fill_(7.0)
+        b.lse.fill_(7.0)
+        b.call(max_q=most, max_len=longest)
+        torch.cuda.synchronize()
+        b.check()
+        assert qkr.last_launch()["kernel_name"] == ("attn_tiles" if kernel in ("tiles", "mixed")
+                                                    else "attn_rows")
+    assert qkr.device_status(reset=True) == 0
+    check()
+    assert qkr.device_status(reset=True) == 0
+    if what == "past":              # a last sequence that begins at T
+        b.cu[5] = b.T + 3
+    elif what == "wholly_past":
+        b.cu[4:] = torch.tensor([b.T + 1, b.T + 3])
+    elif what == "negative":        # before the first row
+        b.cu[0] = -1
+    elif what == "decreasing":
+        b.cu[5] = b.T - 1
+    elif what == "long_empty":      # no new tokens, and a length past max_len
+        b.lens[0] = longest + 1
+    else:
+        b.lens[4] = -1
+    check()
+    assert qkr.device_status(reset=True) == 8
