@@ -439,7 +439,8 @@ typedef struct qkr_cache_desc {
  * cu_q[B] on are not read, and those of out and lse left as they were.
  *
  *   q                bf16 device [T, Hq, D], strides in elements (multiples
- *                    of 8), 16-byte aligned.
+ *                    of 8; the token stride of a single token is not used),
+ *                    16-byte aligned.
  *   out              bf16 device [T, Hq, D], heads dense, 16-byte aligned,
  *                    token stride a multiple of 8.  Must not overlap any input.
  *   lse              nullable fp32 device [T, Hq].

@@ -406,6 +406,10 @@ qkr_status cache_attention(void *stream, const qkr_cache_desc *cache, const void
         return api_fail(QKR_ERR_UNSUPPORTED, "q and out must be 16-byte aligned");
     if (!aligned(lens, 4) || !aligned(cu_q, 4) || !aligned(page_table, 4) || !aligned(lse, 4))
         return api_fail(QKR_ERR_UNSUPPORTED, "page_table, lens, cu_q and lse must be 4-byte aligned");
+    if (s.T == 1) {     // the stride of a single token is never used
+        q_tok_stride = 0;
+        out_tok_stride = s.Hq * s.D;
+    }
     if (q_head_stride < s.D || q_head_stride % 8 || (s.T > 1 && q_tok_stride <= 0) ||
         q_tok_stride % 8 || out_tok_stride < s.Hq * s.D || out_tok_stride % 8)
         return api_fail(QKR_ERR_UNSUPPORTED,

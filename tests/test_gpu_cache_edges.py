@@ -160,3 +160,17 @@ def test_metadata_that_leaves_no_rows_is_reported(kernel, what, fmt):
         b.lens[4] = -1
     check()
     assert qkr.device_status(reset=True) == 8
+
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_single_token_may_have_any_token_stride(fmt):
+    """The token stride of one token is never used: a row of any wider buffer will do."""
+    b = Batch(n=[1], lens=[200], hq=4, hkv=2, D=64, page=16, fmt=fmt, seed=36, pad=0)
+    q = torch.zeros(4 * 64 + 3, dtype=torch.bfloat16, device="cuda").as_strided((1, 4, 64), (259, 64, 1))
+    q.copy_(b.q)
+    assert q.stride(0) % 8
+    b.q = q
+    b.call()
+    torch.cuda.synchronize()
+    b.check()
