@@ -442,7 +442,9 @@ typedef struct qkr_cache_desc {
  *                    of 8; the token stride of a single token is not used),
  *                    16-byte aligned.
  *   out              bf16 device [T, Hq, D], heads dense, 16-byte aligned,
- *                    token stride a multiple of 8.  Must not overlap any input.
+ *                    token stride a multiple of 8.  Must not overlap any input
+ *                    (q and out may be column windows of one buffer with one token
+ *                    stride).
  *   lse              nullable fp32 device [T, Hq].
  *   page_table       int32 device [B, table_stride]; entry [b][i] is the page of
  *                    tokens i*page_size ... of sequence b.
@@ -507,7 +509,8 @@ qkr_status cache_set_rows_q4(void *stream, const qkr_cache_desc *cache, const vo
  * values they stand for (exact): k_out, v_out bf16 device [T, Hkv, D], heads
  * dense.  A row may be named more than once.  A row outside the cache reads as
  * zeros and raises bit 4 of the device status word.  Arguments as
- * cache_set_rows_q4; the outputs must not overlap each other or any input.
+ * cache_set_rows_q4; the outputs must not overlap each other (they may be column
+ * windows of one buffer with one token stride) or any input.
  */
 qkr_status cache_get_rows_q4(void *stream, const qkr_cache_desc *cache, void *k_out, void *v_out,
                              const int64_t *row_idx, int64_t T, int64_t k_tok_stride,

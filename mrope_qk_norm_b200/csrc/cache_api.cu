@@ -28,6 +28,26 @@ bool meet(const Bytes &a, const Bytes &b)
 {
     return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi;
 }
+
+// The rows of a [T, H, D] view: T runs of `width` bytes, `step` apart.
+struct Rows {
+    const void *base;
+    int64_t T, step, width;
+    Bytes all() const { return bytes_of(base, (__int128)(T - 1) * step + width); }
+};
+// Do two views share a byte?  Not if they are column windows of one buffer: the same
+// step, and each row of one between rows of the other.
+bool meet(const Rows &a, const Rows &b)
+{
+    if (!meet(a.all(), b.all()))
+        return false;
+    if (a.step != b.step || a.width > a.step || b.width > b.step)
+        return true;
+    const int64_t diff = (int64_t)(reinterpret_cast<uintptr_t>(b.base) -
+                                   reinterpret_cast<uintptr_t>(a.base)) % a.step;
+    const int64_t at = diff < 0 ? diff + a.step : diff;     // b's row from the start of a's
+    return at < a.width || at + b.width > a.step;
+}
 bool aligned(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 Bytes plane_bytes(const qkr::CachePlane &pl, const qkr::CacheView &c, int64_t row_bytes)
@@ -117,13 +137,14 @@ bool meets_cache(const Bytes &b, const qkr::CacheView &v, bool q4)
                    meet(b, plane_bytes(v.vs, v, v.D / 16))));
 }
 
-// out, lse and the workspace against each other, the inputs and the cache.
-qkr_status check_overlap(const Bytes (&written)[3], const Bytes (&read)[4],
-                         const qkr::CacheView &view, bool q4)
+// out, lse and the workspace against each other, the inputs (q is the first) and the
+// cache; out and q row by row.
+qkr_status check_overlap(const Bytes (&written)[3], const Bytes (&read)[4], const Rows &out,
+                         const Rows &q, const qkr::CacheView &view, bool q4)
 {
     for (int i = 0; i < 3; ++i) {
-        for (const Bytes &r : read)
-            if (meet(written[i], r))
+        for (int j = 0; j < 4; ++j)
+            if (i == 0 && j == 0 ? meet(out, q) : meet(written[i], read[j]))
                 return api_fail(QKR_ERR_UNSUPPORTED,
                                 "out, lse and workspace must not overlap an input");
         for (int j = 0; j < i; ++j)
@@ -423,13 +444,14 @@ qkr_status cache_attention(void *stream, const qkr_cache_desc *cache, const void
                         "max_len (%lld) exceeds the page table: %lld pages of %d tokens",
                         (long long)s.max_len, (long long)table_stride, view.page_size);
 
+    const Rows q_rows = {q, s.T, 2 * q_tok_stride, 2 * ((s.Hq - 1) * q_head_stride + s.D)};
+    const Rows out_rows = {out, s.T, 2 * out_tok_stride, 2 * s.Hq * s.D};
     const Bytes read[4] = {
-        bytes_of(q, 2 * ((s.T - 1) * q_tok_stride + (s.Hq - 1) * q_head_stride + s.D)),
+        q_rows.all(),
         bytes_of(page_table, (__int128)4 * s.B * table_stride), bytes_of(lens, 4 * s.B),
         bytes_of(cu_q, 4 * (s.B + 1))};
-    Bytes written[3] = {bytes_of(out, 2 * ((s.T - 1) * out_tok_stride + s.Hq * s.D)),
-                        bytes_of(lse, 4 * s.T * s.Hq), Bytes()};
-    if ((st = check_overlap(written, read, view, q4)) != QKR_OK)
+    Bytes written[3] = {out_rows.all(), bytes_of(lse, 4 * s.T * s.Hq), Bytes()};
+    if ((st = check_overlap(written, read, out_rows, q_rows, view, q4)) != QKR_OK)
         return st;
     Plan plan;
     if ((st = make_plan(s, view.page_size, &plan)) != QKR_OK)
@@ -441,7 +463,7 @@ qkr_status cache_attention(void *stream, const qkr_cache_desc *cache, const void
         if (!aligned(workspace, 16))
             return api_fail(QKR_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
         written[2] = bytes_of(workspace, plan.ws_bytes);
-        if ((st = check_overlap(written, read, view, q4)) != QKR_OK)
+        if ((st = check_overlap(written, read, out_rows, q_rows, view, q4)) != QKR_OK)
             return st;
     }
 
@@ -525,11 +547,11 @@ static qkr_status rows_q4(void *stream, const qkr_cache_desc *cache, const void 
         v_ts > ((int64_t)1 << 45) / T)
         return api_fail(QKR_ERR_UNSUPPORTED,
                         "token strides must be multiples of 8 and hold a token's heads");
-    const Bytes bk = bytes_of(k, 2 * ((T - 1) * k_ts + row)), bv = bytes_of(v, 2 * ((T - 1) * v_ts + row)),
-                bi = bytes_of(row_idx, 8 * T);
+    const Rows rk = {k, T, 2 * k_ts, 2 * row}, rv = {v, T, 2 * v_ts, 2 * row};
+    const Bytes bk = rk.all(), bv = rv.all(), bi = bytes_of(row_idx, 8 * T);
     if (meets_cache(bk, view, true) || meets_cache(bv, view, true) || meets_cache(bi, view, true))
         return api_fail(QKR_ERR_UNSUPPORTED, "k, v and row_idx must not overlap the cache");
-    if (!set && (meet(bk, bv) || meet(bk, bi) || meet(bv, bi)))
+    if (!set && (meet(rk, rv) || meet(bk, bi) || meet(bv, bi)))
         return api_fail(QKR_ERR_UNSUPPORTED, "k_out, v_out and row_idx must not overlap");
     unsigned *status = nullptr;
     int sms = 0;

@@ -16,3 +16,21 @@ def test_the_token_stride_of_one_token_is_not_used():
                dict(ots=3), dict(ots=1 << 60)):
         assert _attend(T=1, **kw) == OK, _message()
         assert _attend(T=2, **kw) in (E, U)
+
+
+def test_column_windows_of_one_buffer_do_not_overlap():
+    Q, O = BASE + (4 << 30), BASE + (5 << 30)
+    row, at = 2 * 256, lambda n: Q + 2 * n          # Hq * D = 256 elements a token
+    for qts in (512, 768):
+        for off in (256, qts - 256, 256 - qts, qts + 256, -256):
+            assert _attend(qts=qts, ots=qts, out=at(off)) == OK, _message()
+        for off in (0, 8, 248, -8, qts - 248, qts, -248):
+            assert _attend(qts=qts, ots=qts, out=at(off)) == U
+        assert _attend(qts=qts, ots=qts + 256, out=at(256)) == U       # other strides
+    assert _attend(T=1, out=at(256)) == OK and _attend(T=1, out=at(248)) == U
+    assert _attend(out=O, lse=Q + row) == U                             # lse in q
+    for off in (128, 256):                          # Hkv * D = 128
+        assert _rows(get=True, k=Q, v=at(off), kts=384, vts=384) == OK, _message()
+    for off in (0, 120, 264, -120):
+        assert _rows(get=True, k=Q, v=at(off), kts=384, vts=384) == U
+    assert _rows(get=True, k=Q, v=at(128), kts=384, vts=392) == U

@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import mrope_qk_norm_b200 as qkr
-from tests._cache_util import Batch
+from tests._cache_util import Batch, values64
 
 pytestmark = pytest.mark.gpu
 
@@ -174,3 +174,40 @@ def test_a_single_token_may_have_any_token_stride(fmt):
     b.call()
     torch.cuda.synchronize()
     b.check()
+
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n", [1, 50])
+def test_queries_and_result_in_one_buffer(fmt, n):
+    """q and out as column windows of one packed buffer share no element."""
+    b = Batch(n=[n, 1], lens=[300, 40], hq=4, hkv=2, D=64, page=16, fmt=fmt, seed=37)
+    buf = torch.full((b.T, 2 * 4 + 1, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    buf[:, 5:] = b.q
+    b.q, b.out = buf[:, 5:], buf[:, :4]
+    b.call()
+    torch.cuda.synchronize()
+    b.check()
+    with pytest.raises(qkr.QkrError):
+        b.out = buf[:, 2:6]
+        b.call()
+
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_come_back_into_one_buffer(D):
+    """k_out and v_out as column windows of one packed buffer share no element."""
+    T, H, page = 33, 3, 16
+    x = torch.randn((2, T, H, D), device="cuda").to(torch.bfloat16)
+    planes = [torch.empty((4, page, H, w), dtype=t, device="cuda")
+              for w, t in ((D // 2, torch.uint8), (D // 32, torch.bfloat16)) * 2]
+    cache = qkr.cache_desc_q4(*planes)
+    rows = torch.randperm(4 * page)[:T].cuda()
+    qkr.cache_set_rows_q4(x[0], x[1], cache, rows)
+    buf = torch.full((T, 2 * H + 1, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    qkr.cache_get_rows_q4(cache, rows, buf[:, :H], buf[:, H + 1:])
+    assert torch.equal(buf[:, :H].double(), values64(x[0]))
+    assert torch.equal(buf[:, H + 1:].double(), values64(x[1]))
+    assert (buf[:, H] == 7).all()
+    with pytest.raises(qkr.QkrError):
+        qkr.cache_get_rows_q4(cache, rows, buf[:, :H], buf[:, 1:H + 1])
