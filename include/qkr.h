@@ -552,11 +552,13 @@ typedef struct qkr_launch_info {
                                 partner half from another lane); rms: per thread */
     int32_t tokens_per_cta;  /* rope / vit: tokens one CTA covers */
     int32_t heads_per_item;  /* rope: head rows of one token a lane group loads
-                                together */
+                                together; cache_attention: rows (new token x query
+                                head of a KV head) of a block */
     int32_t pipelined;       /* rope: 0 rows loaded straight into registers (item
                                 kernel); 2 rows streamed by every thread into a
                                 cp.async ring (streaming kernel) */
-    int32_t cluster;         /* rms: CTAs per row (cluster size); else 1 */
+    int32_t cluster;         /* rms: CTAs per row (cluster size); cache_attention: CTAs
+                                of the cluster that shares a block's keys; else 1 */
     int32_t block;           /* threads per CTA */
     int32_t direct_angles;   /* rope: 1 if each work item read its (cos, sin) straight
                                 from the fp32 table (16-byte loads), 0 if the angles
@@ -564,7 +566,11 @@ typedef struct qkr_launch_info {
     int32_t overlap;         /* 1 if launched with programmatic stream serialisation
                                 (see qkr_launch_overlap) */
     int32_t stages;          /* streaming kernel: passes in the row ring; cache_attention:
-                                parts the keys of a sequence are split into; else 0 */
+                                few rows: CTAs that share the keys, of a block (a
+                                cluster) or of the whole batch evenly (two launches);
+                                tiles: parts a block's keys are split into at most;
+                                else 0.  A call that takes both kernels records the
+                                tiles kernel and the launches of both. */
     int32_t reserved;        /* 0 */
     int64_t grid;            /* CTAs launched */
     int64_t launches;        /* kernel launches enqueued (0 for an empty call) */

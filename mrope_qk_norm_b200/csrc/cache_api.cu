@@ -508,6 +508,9 @@ qkr_status cache_attention(void *stream, const qkr_cache_desc *cache, const void
             p.page_recip = (((uint64_t)1 << 38) + page_tiles - 1) / page_tiles;
         p.status = plan.status;
         const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+        const int64_t launches = rec.launches;
+        rec = qkr::LaunchRecord();      // the last kernel's own shape, all launches
+        rec.launches = launches;
         if (which && p.scale_log2 == 0.f)
             p.scale_log2 = FLT_MIN;  // masked scores are -infinity times the scale
         e = which ? qkr::launch_attn_tiles(p, q4, cs, &rec) : qkr::launch_attn_rows(p, q4, cs, &rec);

@@ -211,3 +211,15 @@ def test_rows_come_back_into_one_buffer(D):
     assert (buf[:, H] == 7).all()
     with pytest.raises(qkr.QkrError):
         qkr.cache_get_rows_q4(cache, rows, buf[:, :H], buf[:, 1:H + 1])
+
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_last_launch_of_a_mixed_call(fmt):
+    """What is recorded is the tiles launch's own, and all launches are counted."""
+    b = Batch(n=[1, 90, 2], lens=[40, 300, 50], hq=4, hkv=2, D=64, page=16, fmt=fmt, seed=35)
+    b.call()
+    torch.cuda.synchronize()
+    info = qkr.last_launch()
+    assert info["kernel_name"] == "attn_tiles" and info["launches"] >= 2
+    assert info["cluster"] == 1
