@@ -223,3 +223,18 @@ def test_last_launch_of_a_mixed_call(fmt):
     info = qkr.last_launch()
     assert info["kernel_name"] == "attn_tiles" and info["launches"] >= 2
     assert info["cluster"] == 1
+
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_even_shares_cut_a_long_sequence(fmt):
+    """The shares computed from the lengths: the long sequence's keys lie in many CTAs."""
+    b = Batch(n=[1, 1], lens=[9000, 33], hq=8, hkv=1, D=128, page=64, fmt=fmt, seed=39)
+    b.call()
+    torch.cuda.synchronize()
+    info = qkr.last_launch()
+    ctas, tile, piece = info["stages"], 64, (128 if fmt == "bf16" else 512) // 64
+    work = sum(piece + -(-m // tile) for m in b.L)
+    quota = max(-(-work // ctas), 128 // tile)
+    assert info["launches"] == 2 and -(-9000 // tile) > 2 * quota
+    b.check()
