@@ -489,9 +489,9 @@ qkr_status cache_attention_workspace(const qkr_cache_desc *cache, int64_t T, int
  * already, by mrope_apply say).  Token t goes to flat row row_idx[t].  Per
  * group of 32 elements: e = the element of largest magnitude (the negative one
  * when both signs tie), s = e / -8 with its magnitude rounded up to 5 significant
- * bits (at most 31 * 2^120, so that 8s stays finite), code = clamp(rint(x / s), -8, 7) + 8 (ties to even; 8 where s is 0).
- * A group with an
- * infinity or a NaN reads back as NaN throughout.
+ * bits (below 2^-126 to a multiple of 2^-130; at most 31 * 2^120, so that 8s stays
+ * finite), code = clamp(rint(x / s), -8, 7) + 8 (ties to even; 8 where s is 0).  A
+ * group with an infinity or a NaN reads back as NaN throughout.
  *
  *   k, v             bf16 device [T, Hkv, D], heads dense, token strides in
  *                    elements (multiples of 8), 16-byte aligned; T * Hkv <= 2^30.

@@ -67,7 +67,9 @@ __device__ __forceinline__ uint8_t *place(const CachePlane &pl, const Where &w)
 }
 
 // The scale of a group with extremes hi and lo, its magnitude at most 31 * 2^120
-// (the largest of 5 bits whose eightfold is a finite bf16 number).
+// (the largest of 5 bits whose eightfold is a finite bf16 number).  The carry rounds a
+// subnormal e up to a multiple of 2^-130, with fewer significant bits: 3 bits times it are
+// still a multiple of 2^-133, so a bf16 number.
 __device__ __forceinline__ float group_scale(float hi, float lo)
 {
     const float e = (-lo >= hi ? lo : hi) * -0.125f;

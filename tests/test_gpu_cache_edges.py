@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import mrope_qk_norm_b200 as qkr
-from tests._cache_util import Batch, values64
+from tests._cache_util import Batch, pack, values64
 
 pytestmark = pytest.mark.gpu
 
@@ -238,3 +238,43 @@ def test_even_shares_cut_a_long_sequence(fmt):
     quota = max(-(-work // ctas), 128 // tile)
     assert info["launches"] == 2 and -(-9000 // tile) > 2 * quota
     b.check()
+
+
+
+def test_scales_below_the_normal_numbers():
+    """Groups whose scale is subnormal: rounded up to a multiple of 2^-130, bit for bit.
+    Every positive and negative extreme below 2^-121, beside other elements of the group."""
+    D, page = 128, 64
+    top = torch.arange(1, 0x0300, dtype=torch.int16)      # 2^-133 .. 2^-121
+    x = torch.zeros((2 * len(top), 32), dtype=torch.int16)
+    x[:, 0] = torch.cat([top, top | -0x8000])
+    g = torch.Generator().manual_seed(38)
+    for i in range(1, 32):          # magnitudes up to the extreme's, either sign
+        part = (x[:, 0] & 0x7fff).float() * torch.rand(len(x), generator=g)
+        sign = torch.randint(0, 2, (len(x),), generator=g).to(torch.int16) * -0x8000
+        x[:, i] = part.to(torch.int16) | sign
+    x = torch.cat([x, torch.zeros((-len(x) % 4, 32), dtype=torch.int16)])
+    k = x.view(torch.bfloat16).view(-1, 1, D).cuda()
+    T = len(k)
+    planes = [torch.empty((-(-T // page), page, 1, w), dtype=t, device="cuda")
+              for w, t in ((D // 2, torch.uint8), (D // 32, torch.bfloat16)) * 2]
+    cache = qkr.cache_desc_q4(*planes)
+    rows = torch.arange(T, device="cuda")
+    qkr.cache_set_rows_q4(k, k, cache, rows)
+    # the definition, with the grid of the subnormal scales
+    y = k.cpu().double().view(T, 1, 4, 32)
+    big = y.abs().amax(-1, keepdim=True)
+    mant, expo = torch.frexp(big / 8)
+    s = torch.ldexp(torch.ceil(mant * 32) / 32, expo)
+    s = torch.where(big / 8 < 2.0 ** -126, torch.ceil(big / 8 * 2.0 ** 130) * 2.0 ** -130, s)
+    s = torch.where((y == -big).any(-1, keepdim=True), s, -s)
+    c = torch.round(torch.where(s == 0, 0.0, y / torch.where(s == 0, 1.0, s))).clamp(-8, 7)
+    codes = (c + 8).to(torch.uint8).view(T, 1, D).cuda()
+    want = (c * s).view(T, 1, D)
+    assert torch.equal(planes[0].view(-1, 1, D // 2)[:T], pack(codes, False))
+    assert torch.equal(planes[2].view(-1, 1, D // 2)[:T], pack(codes, True))
+    for i in (1, 3):
+        assert torch.equal(planes[i].view(-1, 1, 4)[:T].double().cpu(), s.squeeze(-1))
+    ko, vo = torch.empty_like(k), torch.empty_like(k)
+    qkr.cache_get_rows_q4(cache, rows, ko, vo)
+    assert torch.equal(ko.double().cpu(), want) and torch.equal(vo.double().cpu(), want)
