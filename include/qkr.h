@@ -453,7 +453,7 @@ typedef struct qkr_cache_desc {
  *                    max_len <= table_stride * page_size.  B <= 2^16,
  *                    T * Hq < 2^31, max_len <= 2^29.  They set the launch
  *                    shape only, so a captured graph serves any lengths up to them.
- *   scale            finite.   window, n_sink >= 0.
+ *   scale            at most 2^127 in magnitude.   window, n_sink >= 0.
  *   workspace        device scratch of cache_attention_workspace() bytes, 16-byte
  *                    aligned (may be NULL where that is 0).  It carries nothing from
  *                    call to call; calls that may run at the same time (other

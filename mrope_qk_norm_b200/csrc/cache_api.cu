@@ -417,8 +417,10 @@ qkr_status cache_attention(void *stream, const qkr_cache_desc *cache, const void
     Sizes s = {T, Hq, cache->Hkv, cache->D, B, max_q, max_len, window, n_sink, q4};
     if ((st = check_sizes(s)) != QKR_OK)
         return st;
-    if (!std::isfinite(scale))
-        return api_fail(QKR_ERR_INVALID_ARG, "scale must be finite");
+    // the softmax works in powers of two
+    const float scale_log2 = (float)((double)scale * 1.4426950408889634);
+    if (!std::isfinite(scale_log2))
+        return api_fail(QKR_ERR_INVALID_ARG, "scale must be finite, at most 2^127 in magnitude");
     if (s.T == 0 || s.B == 0 || s.max_q == 0)
         return api_done(qkr::LaunchRecord());
     if (!q || !out || !lens || !cu_q || (s.max_len && !page_table))
@@ -492,7 +494,7 @@ qkr_status cache_attention(void *stream, const qkr_cache_desc *cache, const void
         p.max_len = (int)s.max_len;
         p.window = (int)s.window;
         p.n_sink = (int)s.n_sink;
-        p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+        p.scale_log2 = scale_log2;
         p.ws_o = static_cast<float *>(workspace);
         const int64_t kept = p.ctas ? 2 * (int64_t)p.ctas * p.rows : (int64_t)p.nsplit * s.T * s.Hq;
         p.ws_ml = reinterpret_cast<float2 *>(p.ws_o + kept * s.D);

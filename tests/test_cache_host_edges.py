@@ -34,3 +34,11 @@ def test_column_windows_of_one_buffer_do_not_overlap():
     for off in (0, 120, 264, -120):
         assert _rows(get=True, k=Q, v=at(off), kts=384, vts=384) == U
     assert _rows(get=True, k=Q, v=at(128), kts=384, vts=392) == U
+
+
+def test_a_scale_beyond_the_range_is_refused():
+    """scale * log2(e) has to be a finite fp32 number."""
+    for x in (2.0 ** 127, -2.0 ** 127, 2.3e38, 1e-45, 0.0):
+        assert _attend(scale=x) == OK, _message()
+    for x in (2.4e38, -3.4e38):
+        assert _attend(scale=x) == E and "scale" in _message()
