@@ -1,7 +1,6 @@
 // cache_api.cu -- C ABI of the paged cache: validation, launch shapes, launch.
 
 #include <atomic>
-#include <cfloat>
 #include <climits>
 #include <cmath>
 
@@ -514,7 +513,8 @@ qkr_status cache_attention(void *stream, const qkr_cache_desc *cache, const void
         rec = qkr::LaunchRecord();      // the last kernel's own shape, all launches
         rec.launches = launches;
         if (which && p.scale_log2 == 0.f)
-            p.scale_log2 = FLT_MIN;  // masked scores are -infinity times the scale
+            p.scale_log2 = 0x1p-149f;  // masked scores are -infinity times the scale, and
+                                       // any finite score times this is below 2^-21
         e = which ? qkr::launch_attn_tiles(p, q4, cs, &rec) : qkr::launch_attn_rows(p, q4, cs, &rec);
         if (e != cudaSuccess)
             return cuda_fail(e, "cache attention launch");

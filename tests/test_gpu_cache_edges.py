@@ -278,3 +278,25 @@ def test_scales_below_the_normal_numbers():
     ko, vo = torch.empty_like(k), torch.empty_like(k)
     qkr.cache_get_rows_q4(cache, rows, ko, vo)
     assert torch.equal(ko.double().cpu(), want) and torch.equal(vo.double().cpu(), want)
+
+
+def _scaled(b, i, f):
+    """Multiplies the K (0) or V (1) rows of a batch by a power of two."""
+    pl = b.planes[i if b.fmt == "bf16" else 2 * i + 1]
+    pl.copy_((pl.double() * f).to(torch.bfloat16))
+    if i:
+        b.v64 *= f
+    else:
+        b.k64 *= f
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_scale_of_zero_takes_the_mean_of_any_scores(fmt):
+    """Scores of some 2^125 times zero are zero."""
+    b = Batch(n=[1, 40], lens=[300, 100], hq=4, hkv=2, D=64, page=16, fmt=fmt, seed=40,
+              poison=False)
+    _scaled(b, 0, 2.0 ** 60)
+    b.q = b.q * 2.0 ** 60
+    b.call(scale=0.0)
+    torch.cuda.synchronize()
+    b.check(scale=0.0)
