@@ -462,9 +462,12 @@ typedef struct qkr_cache_desc {
  * [0, max_len], a cu_q entry outside [0, T], or more than max_q new tokens is
  * clamped, a cu_q entry below the one before it leaves a sequence no new tokens, a page id outside the cache reads as rows of zeros, and each raises
  * bit 8 of the device status word.
- * The maximum, the sum and the output are held in fp32 and divided at the end, so
- * seen values of V beyond 2^100 in magnitude can overflow; the weights exp(s - m)
- * are rounded to bf16 for their product with V, and out once at the end.
+ * Scores, the maximum, the sum and the output are held in fp32.  A weight is taken
+ * against a reference up to 2^8 below the maximum and divided at the end, so seen values
+ * of V beyond 2^120 over the number of seen keys (2^110 at most) can overflow in
+ * magnitude, and over a 4-bit cache elements of q beyond 2^115.  The weights exp(s - m)
+ * are rounded to bf16 for their product with V (over a 4-bit cache with few rows a
+ * sequence, after V's scale has been multiplied in), and out once at the end.
  * Enqueues one kernel for sequences of few rows (new tokens times query heads of a
  * KV head, up to 16) or of many, or one for each where both can stand side by
  * side, and after either one that joins the parts of a split axis.

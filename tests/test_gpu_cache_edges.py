@@ -300,3 +300,19 @@ def test_a_scale_of_zero_takes_the_mean_of_any_scores(fmt):
     b.call(scale=0.0)
     torch.cuda.synchronize()
     b.check(scale=0.0)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_largest_values_and_queries(fmt, D):
+    """Values just below 2^120 over the number of keys, queries just below 2^114."""
+    b = Batch(n=[1, 40, 5], lens=[250, 100, 200], hq=4, hkv=2, D=D, page=16, fmt=fmt, seed=41,
+              poison=False)
+    _scaled(b, 1, 2.0 ** 107)                       # a few times that: up to 2^110
+    assert 2.0 ** 109 < b.v64.abs().max() < 2.0 ** 110
+    b.q = b.q * 2.0 ** 111
+    assert 2.0 ** 112 < b.q[:46].abs().max() < 2.0 ** 114
+    scale = D ** -0.5 * 2.0 ** -111
+    b.call(scale=scale)
+    torch.cuda.synchronize()
+    b.check(scale=scale)
