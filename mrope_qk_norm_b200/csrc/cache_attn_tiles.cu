@@ -62,11 +62,11 @@ constexpr int tiles_threads(bool q4) { return 32 * (kSoftWarps + (q4 ? 12 : 4));
 constexpr int kTile = 128;               // keys of a tile, rows of a tile
 constexpr float kSlack = 8.f;
 // One pair of exponentials in 8 on the FMA pipe (8192-token prompt: 251 us; every
-// fourth 257, none 257).
+// fourth 257, none 257, with a degree less and launches apart; the degree costs 0.5%).
 constexpr int kPolyEvery = 8;
-constexpr float kExpC0 = 0.9999992847442627f, kExpC1 = 0.6931217908859253f,
-                kExpC2 = 0.240247443318367f, kExpC3 = 0.05591785907745361f,
-                kExpC4 = 0.009570100344717503f;
+constexpr float kExpC0 = 1.0000000716546416f, kExpC1 = 0.6931469670652649f,
+                kExpC2 = 0.2402211972396918f, kExpC3 = 0.0555071327287539f,
+                kExpC4 = 0.0096755413310214f, kExpC5 = 0.0013276472167820f;
 // A wait asks so often at most, 8.6 s (an asking that fails takes some 4 us).  Roles that
 // run ahead sleep in between (their polls would take issue slots from the others).
 constexpr uint32_t kWaitLimit = 1u << 21;
@@ -285,9 +285,9 @@ __device__ __forceinline__ uint64_t exp2_mufu2(uint64_t x)
 
 // 2^x for x <= 2^7 on the FMA pipe: x = n + f with n the nearest integer (the
 // rounding of x + 1.5 * 2^23, whose low bits are n), 2^f by the polynomial of
-// degree 4 with the least relative error on [-1/2, 1/2] (Remez; 2.7e-6, a
-// thousandth of the bf16 rounding that follows), n added to the exponent; 0
-// below x = -126, as the instruction gives.
+// degree 5 with the least relative error on [-1/2, 1/2] (Remez; 7.5e-8, 2.1e-7 with
+// fp32's roundings, the instruction's accuracy: l and the lse sum it unrounded), n
+// added to the exponent; 0 below x = -126, as the instruction gives.
 __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x)
 {
     const uint64_t big = pack_f2(12582912.f, 12582912.f), nbig = pack_f2(-12582912.f, -12582912.f);
@@ -295,7 +295,8 @@ __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x)
     x = pack_f2(fmaxf(lo, -126.f), fmaxf(hi, -126.f));
     const uint64_t t = add_f2(x, big);
     const uint64_t f = fma_f2(add_f2(t, nbig), pack_f2(-1.f, -1.f), x);
-    uint64_t r = pack_f2(kExpC4, kExpC4);
+    uint64_t r = pack_f2(kExpC5, kExpC5);
+    r = fma_f2(r, f, pack_f2(kExpC4, kExpC4));
     r = fma_f2(r, f, pack_f2(kExpC3, kExpC3));
     r = fma_f2(r, f, pack_f2(kExpC2, kExpC2));
     r = fma_f2(r, f, pack_f2(kExpC1, kExpC1));
