@@ -107,8 +107,10 @@ struct Rows {
     static constexpr int kPart = kKeys * (Q4 ? DP / 2 : DP * 2);   // K or V of a stage
     static constexpr int kStageBytes = 2 * (kPart + kKeys * kScale);
     static constexpr int kStages = Q4 ? (DP == 64 ? 4 : 3) : (DP == 64 ? 4 : (NT == 1 ? 3 : 2));
-    // CTAs an SM holds (by shared memory and registers)
-    static constexpr int kCtas = DP == 128 ? (Q4 && NT == 1 ? 3 : 2) : (Q4 && NT == 1 ? 4 : 3);
+    // CTAs an SM holds (by shared memory and registers).  (bf16, D = 64, two tiles of rows:
+    // 32 sequences of 16384, 16 heads over one: 44 us with 2 of 4 stages, 46 with 3 of 3.)
+    static constexpr int kCtas = DP == 128 ? (Q4 && NT == 1 ? 3 : 2)
+                                           : (NT == 1 ? (Q4 ? 4 : 3) : (Q4 ? 3 : 2));
 };
 
 // After the ring, which the copies want on a 1024-byte boundary.
@@ -1201,6 +1203,9 @@ cudaError_t rows_launch(const AttnParams &p, cudaStream_t stream, LaunchRecord *
 {
     using R = Rows<DP, Q4, NT>;
     constexpr int smem = R::kStages * R::kStageBytes + (int)sizeof(RowsShared<DP, NT>);
+    // even shares are made for CTAs that all run at once (an SM has 228 KB; 1 KB a CTA
+    // is the system's)
+    static_assert(R::kCtas * (smem + 1024) <= 228 * 1024);
     CacheMaps maps;
     auto fn = p.ctas ? attn_rows_kernel<DP, NT, Q4> : attn_cluster_kernel<DP, NT, Q4>;
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(fn), smem);

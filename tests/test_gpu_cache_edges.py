@@ -316,3 +316,24 @@ def test_largest_values_and_queries(fmt, D):
     b.call(scale=scale)
     torch.cuda.synchronize()
     b.check(scale=scale)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("hq", [4, 8, 16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_even_shares_for_resident_ctas(fmt, D, hq):
+    """The CTAs that share a batch's keys all fit the SMs at once: by shared memory, 3 or 4
+    CTAs of up to 8 rows of 64 dims, 2 or 3 otherwise."""
+    b = Batch(n=[1] * 4, lens=[5000, 17, 800, 4000], hq=hq, hkv=1, D=D, page=64, fmt=fmt, seed=42)
+    b.call()
+    torch.cuda.synchronize()
+    info = qkr.last_launch()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    # the ring (K and V of a stage, and scales) and the four warps' outputs in fp32
+    keys, row = (64, 2 * D) if fmt == "bf16" else (128, D // 2 + D // 16)
+    stages = 4 if D == 64 else (2 if fmt == "bf16" and hq > 8 else 3)
+    rows = 8 if hq <= 8 else 16
+    smem = stages * 2 * keys * row + 4 * rows * (D + 4) * 4
+    assert info["launches"] == 2 and info["grid"] % sms == 0
+    assert info["grid"] // sms * (smem + 1024) <= 228 * 1024
+    b.check()
