@@ -337,3 +337,44 @@ def test_even_shares_for_resident_ctas(fmt, D, hq):
     assert info["launches"] == 2 and info["grid"] % sms == 0
     assert info["grid"] // sms * (smem + 1024) <= 228 * 1024
     b.check()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_most_sequences_of_a_call(fmt):
+    """2^16 sequences, most of one key, some without new tokens."""
+    B = 1 << 16
+    n = [0 if i % 7 == 3 else 1 for i in range(B)]
+    cu = torch.tensor([0] + n).cumsum(0).to(torch.int32)
+    T, P, page, D = int(cu[-1]), 64, 16, 64
+    g = torch.Generator().manual_seed(43)
+    k, v = (torch.randn((P, page, 1, D), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    if fmt == "bf16":
+        cache = qkr.cache_desc(k, v)
+    else:
+        planes = [torch.empty((P, page, 1, w), dtype=t, device="cuda")
+                  for w, t in ((D // 2, torch.uint8), (D // 32, torch.bfloat16)) * 2]
+        cache = qkr.cache_desc_q4(*planes)
+        every = torch.arange(P * page, device="cuda")
+        qkr.cache_set_rows_q4(k.view(-1, 1, D), v.view(-1, 1, D), cache, every)
+        qkr.cache_get_rows_q4(cache, every, k.view(-1, 1, D), v.view(-1, 1, D))
+    table = torch.randint(0, P, (B, 1), generator=g).to(torch.int32)
+    lens = torch.ones(B, dtype=torch.int32)
+    lens[100], lens[B - 1] = 16, 9
+    q = torch.randn((T, 2, D), generator=g).to(torch.bfloat16).cuda()
+    out = torch.full_like(q, 7.0)
+    ws = torch.empty(qkr.cache_attention_workspace(q, cache, B, 1, 16), dtype=torch.uint8,
+                     device="cuda")
+    qkr.cache_attention(q, cache, out, table.cuda(), lens.cuda(), cu.cuda(), 1, 16, workspace=ws)
+    seq = torch.arange(B)[torch.tensor(n) > 0]
+    # one key: its value row, whatever the query
+    want = v[table[seq, 0].long().cuda(), 0].expand(-1, 2, -1).clone()
+    one = lens[seq].cuda() == 1
+    torch.cuda.synchronize()
+    assert torch.equal(out[one], want[one])
+    for b in (100, B - 1):
+        kk, vv = (x[int(table[b, 0]), :int(lens[b]), 0].double() for x in (k, v))
+        t = int(cu[b])
+        w = torch.softmax(q[t].double() @ kk.T * D ** -0.5, -1)
+        # the weights' rounding and the result's, and 2^-10 for all that is fp32
+        assert ((out[t].double() - w @ vv).abs() <= (w @ vv.abs()) * (2 * 2.0 ** -8 + 2.0 ** -10)).all()
+    assert qkr.device_status(reset=True) == 0
