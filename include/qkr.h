@@ -467,7 +467,9 @@ typedef struct qkr_cache_desc {
  * of V beyond 2^120 over the number of seen keys (2^110 at most) can overflow in
  * magnitude, and over a 4-bit cache elements of q beyond 2^115.  The weights exp(s - m)
  * are rounded to bf16 for their product with V (over a 4-bit cache with few rows a
- * sequence, after V's scale has been multiplied in), and out once at the end.
+ * sequence, after V's scale has been multiplied in), and out once at the end.  Over a
+ * 4-bit cache with few rows a sequence the sums run on codes with an offset, at most 31
+ * steps of a scale, which costs fp32 rounding at that size: in out 2^-17 of V's scale.
  * Enqueues one kernel for sequences of few rows (new tokens times query heads of a
  * KV head, up to 16) or of many, or one for each where both can stand side by
  * side, and after either one that joins the parts of a split axis.

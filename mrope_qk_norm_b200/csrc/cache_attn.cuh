@@ -26,6 +26,15 @@ __device__ __forceinline__ uint32_t nibbles(uint32_t w, int i)
     return r;
 }
 
+// The same as (16 + n_i, 16 + n_{i+4}), where sums run on the numbers with their offset.
+__device__ __forceinline__ uint32_t nibbles16(uint32_t w, int i)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;"
+        : "=r"(r) : "r"(i ? w >> (4 * i - 3) : w << 3), "r"(0x00780078u), "r"(0x41804180u));
+    return r;
+}
+
 __device__ __forceinline__ bool nonfinite2(uint32_t w)  // either bf16 of the word
 {
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;

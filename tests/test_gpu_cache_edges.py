@@ -378,3 +378,37 @@ def test_most_sequences_of_a_call(fmt):
         # the weights' rounding and the result's, and 2^-10 for all that is fp32
         assert ((out[t].double() - w @ vv).abs() <= (w @ vv.abs()) * (2 * 2.0 ** -8 + 2.0 ** -10)).all()
     assert qkr.device_status(reset=True) == 0
+
+
+@pytest.mark.parametrize("n", [1, 2])
+@pytest.mark.parametrize("D", [64, 128])
+def test_zero_codes_under_a_large_weight(D, n):
+    """4-bit rows whose scores let one key have nearly all the weight: where its values
+    are zero, its offset leaves little in the fp32 sums.
+
+    A code's products run on 16 + nibble, 31 at most, and on -24; each of a tile's two
+    sums rounds (or cuts) to fp32, 2^-23 relative to 31 times its keys' weights times
+    scales, so all tiles together are off by 2^-22 * 31 times their weighted mean."""
+    lens = [max(n, (37 * i) % 400) for i in range(40)]
+    b = Batch(n=[n] * 40, lens=lens, hq=8, hkv=2, D=D, page=32, fmt="q4", seed=44, poison=False,
+              pad=0)
+    b.call(scale=0.5)
+    torch.cuda.synchronize()
+    for s, L in enumerate(lens):
+        k, v = b.rows64(s)
+        for h in range(8):
+            for i in range(n):
+                q = b.q[s * n + i, h].double()
+                see = L - n + i + 1
+                kk, vv = k[:see, h // 4], v[:see, h // 4]
+                z = 0.5 * (kk @ q)
+                w = torch.softmax(z, -1)
+                # scores: 31 steps of the scale a product, fp32 sums of D of them
+                step = kk.reshape(see, -1, 32).abs().amax(-1) / 7
+                mag = (q.abs().reshape(-1, 32).sum(-1) * 31 * step).sum(-1).max() * 0.5
+                rel = 2.0 ** -8 + 2 * mag * 2.0 ** -20 + 2 * 2.0 ** -16
+                tol = 1.01 * rel * (w @ vv.abs()) + (w @ vv).abs() * 2.0 ** -8
+                scales = b.planes[3][b.table[s].long()].flatten(0, 1)[:see, h // 4].double().abs()
+                tol = tol + 31 * 2.0 ** -22 * (w @ scales).repeat_interleave(32)
+                err = (b.out[s * n + i, h].double() - w @ vv).abs()
+                assert (err <= tol).all(), (s, h, i, (err / tol).max().item())
