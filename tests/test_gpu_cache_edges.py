@@ -1,4 +1,7 @@
 """The cache operators at the edges of what include/qkr.h allows."""
+import math
+import random
+
 import pytest
 import torch
 
@@ -412,3 +415,79 @@ def test_zero_codes_under_a_large_weight(D, n):
                 tol = tol + 31 * 2.0 ** -22 * (w @ scales).repeat_interleave(32)
                 err = (b.out[s * n + i, h].double() - w @ vv).abs()
                 assert (err <= tol).all(), (s, h, i, (err / tol).max().item())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n", [[2, 1], [300, 0, 5]])
+def test_an_empty_cache_needs_no_page_table(fmt, n):
+    """max_len 0: nothing is looked up, every row is zero."""
+    b = Batch(n=n, lens=[0] * len(n), hq=4, hkv=2, D=64, page=16, fmt=fmt, seed=45)
+    b.table = b.table[:, :0]
+    b.call()
+    torch.cuda.synchronize()
+    b.check()
+    assert qkr.device_status(reset=True) == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_captured_mixed_step_serves_any_lengths(fmt):
+    """One captured call with both kernels and their joins, replayed for other numbers of
+    new tokens and lengths, beside eager calls on another stream."""
+    most, longest = [130, 130, 60, 8], [2500, 700, 300, 1000]
+    b = Batch(n=most, lens=longest, hq=4, hkv=2, D=64, page=16, fmt=fmt, seed=46, poison=False,
+              pad=40)
+    other = Batch(n=[1, 70], lens=[900, 300], hq=4, hkv=2, D=128, page=32, fmt=fmt, seed=47)
+    ws = b.call(max_q=130)
+    side_ws = other.call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.call(max_q=130, max_len=2500, workspace=ws)
+    side = torch.cuda.Stream()
+    for n, lens in (([1, 1, 1, 1], [2400, 5, 300, 999]), ([0, 130, 0, 2], [7, 131, 0, 2]),
+                    (most, longest), ([3, 129, 17, 0], [2500, 700, 17, 0]), ([130, 0, 5, 0], [90, 1, 4, 2])):
+        b.n, b.L = n, lens
+        b.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        b.cu.copy_(torch.tensor([0] + n).cumsum(0).to(torch.int32))
+        b.out_buf.fill_(7.0)
+        b.lse.fill_(7.0)
+        other.out_buf.fill_(7.0)
+        other.lse.fill_(7.0)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            graph.replay()
+            other.call(stream=side, workspace=side_ws)
+        torch.cuda.synchronize()
+        b.check()
+        other.check()
+    assert qkr.device_status(reset=True) == 0
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_calls(seed):
+    """Formats, sizes, head layouts, lengths, windows and host bounds drawn together."""
+    rng = random.Random(seed)
+
+    def log_int(lo, hi):
+        return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+    for it in range(4):
+        fmt = FORMATS[it % 2]
+        D = rng.choice([64, 128]) if fmt == "q4" else rng.choice([8, 24, 40, 64, 72, 96, 104, 128])
+        hkv, G = rng.choice([1, 1, 2, 3, 5]), rng.choice([1, 2, 3, 4, 5, 7, 8, 11, 16, 17, 33])
+        B, page = log_int(1, 12), 16 * rng.choice([1, 1, 2, 3, 4, 5, 8, 9, 16])
+        top = rng.choice([1, 5, 200, 400])
+        n = [rng.choice([0, 1, log_int(1, top)]) for _ in range(B)]
+        n[0] = max(n[0], 1)
+        lens = [max(k, rng.choice([k, log_int(1, 3000 if B < 4 else 600)])) for k in n]
+        if rng.random() < 0.2:
+            lens[-1] = n[-1] // 2       # fewer tokens in the cache than new ones
+        window, sink = rng.choice([(0, 0), (log_int(1, 700), rng.choice([0, 1, 4, 17, 600]))])
+        b = Batch(n=n, lens=lens, hq=hkv * G, hkv=hkv, D=D, page=page, window=window, sink=sink,
+                  fmt=fmt, order=rng.choice(["nhd", "hnd"]), seed=seed, pad=rng.choice([0, 3, 20]),
+                  poison=rng.random() < 0.8)
+        scale = rng.choice([None, 0.0, -0.1])
+        b.call(scale=scale, max_q=max(n) + rng.choice([0, 1, 30]),
+               max_len=min(b.table.shape[1] * page, max(max(lens), 1) + rng.choice([0, 1, page])))
+        torch.cuda.synchronize()
+        b.check(scale=scale)
+    assert qkr.device_status(reset=True) == 0
