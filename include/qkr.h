@@ -451,7 +451,8 @@ typedef struct qkr_cache_desc {
  *   lens             int32 device [B];  cu_q int32 device [B + 1], nondecreasing.
  *   max_q, max_len   host bounds of the new tokens of a sequence and of lens[b];
  *                    max_len <= table_stride * page_size.  B <= 2^16,
- *                    T * Hq < 2^31, max_len <= 2^29.  They set the launch
+ *                    T * Hq < 2^31, max_len <= 2^29, and at most 2^23 blocks a
+ *                    launch: B * Hkv + T * Hq / 256 is less.  They set the launch
  *                    shape only, so a captured graph serves any lengths up to them.
  *   scale            at most 2^127 in magnitude.   window, n_sink >= 0.
  *   workspace        device scratch of cache_attention_workspace() bytes, 16-byte

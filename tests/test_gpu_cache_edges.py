@@ -1,4 +1,5 @@
 """The cache operators at the edges of what include/qkr.h allows."""
+import ctypes
 import math
 import random
 
@@ -491,3 +492,16 @@ def test_random_calls(seed):
         torch.cuda.synchronize()
         b.check(scale=scale)
     assert qkr.device_status(reset=True) == 0
+
+
+def test_more_blocks_than_a_launch_takes_are_refused():
+    c = qkr.CacheDesc(format=qkr.CACHE_BF16, page_size=16, n_pages=1, Hkv=256, D=64)
+    n = ctypes.c_int64(-1)
+
+    def need(T, B, max_q):
+        return qkr.lib().cache_attention_workspace(ctypes.byref(c), T, 256, B, max_q, 64, 0, 0,
+                                                   ctypes.byref(n))
+    assert need(1 << 16, 1 << 16, 1) == qkr.QKR_ERR_UNSUPPORTED       # 2^24 blocks of few rows
+    assert need(1 << 15, (1 << 15) - 1, 1) == qkr.QKR_OK
+    assert need(1 << 20, 1 << 15, 1 << 10) == qkr.QKR_ERR_UNSUPPORTED  # and of many
+    assert need(1 << 20, 1 << 14, 1 << 10) == qkr.QKR_OK
