@@ -25,9 +25,11 @@
 // operands into registers (two sequences of 130,000 tokens in 4 bits, 8 KV heads of
 // 128: 141 us, three warps a scheduler each waiting for its own loads; now 95), and
 // with a feeding warp that copied 16 bytes a lane that warp was the bound (100,000
-// tokens in bf16: 344 us against 146; now 134, 95% of the copy rate).  4 bits is
-// bound by instructions: about 400 a 16 keys, half of them on the half-rate integer
-// pipe, which nibbles keep busy for as long as HBM needs for the bytes.
+// tokens in bf16: 344 us against 146; now 134, 94% of the copy rate).  In 4 bits
+// no unit is full (issue slots 54%, integer pipe 52%, DRAM 40%, tensor pipe 26%): a warp's
+// 400 instructions a 16 keys are one chain from nibbles to the second product, and three
+// computing warps a scheduler (128 registers, with spills) leave 45% of the cycles
+// without one that can issue.
 //
 // Who takes which keys.  Much work: as many CTAs as stay resident, each with the
 // same number of tiles of the row (sequence, KV head, tile), found on the device

@@ -30,7 +30,7 @@
 // instead of 2048 (a tile's softmax, 1700 to 2100 clocks, and its two products follow
 // one another, and two tiles hide only part of that), and some 18,000 clocks a block
 // for setting up and writing out.  A prompt of 8192 tokens, 16 heads over 8 of 128:
-// 289 us, 0.95 PFLOP/s (250 us and 1.1 where launches stand apart and the clock is
+// 288 us, 0.95 PFLOP/s (250 us and 1.1 where launches stand apart and the clock is
 // higher).
 //
 // The running maximum is a reference that moves only when a score exceeds it by
